@@ -229,6 +229,91 @@ PARO_API paro_status paro_rotate_w4a4_linear(const uint16_t* d_x, int K, const u
                                              paro_stream_t stream);
 
 /*
+ * The 8-bit path, for linears that are kept at 8 bits beside the INT4 ones: int8
+ * codes with one fp32 scale for each row (token or output channel), the RMS norm
+ * that gives them, and the int8 x int8 linears on them.
+ *
+ * Row codes: for a row v of d values with a = max |v_c|, q_c is the whole number
+ * nearest to 127 v_c / a, ties to the even one (decided exactly, so codes do not
+ * depend on the order of any sum), and the scale is a / 127; a code stands for
+ * code * scale.  An all-zero row has codes 0 and scale 1; a row with an infinity
+ * or NaN has codes 0 and scale NaN, so that the outputs of that row, and of no
+ * other, are NaN.
+ *
+ * Activations, gains, biases and outputs are bf16 or fp16 by `dtype`; rows are
+ * dense; pointers are 16-byte aligned (scales 4, bias 2).
+ */
+typedef enum { PARO_BF16 = 0, PARO_FP16 = 1 } paro_dtype;
+
+/*
+ * Row codes of activations.  d_x: [M][d], 1 <= d <= 49152; d_q: int8 [M][d];
+ * d_sx: fp32 [M].  The outputs overlap neither each other nor d_x.
+ */
+PARO_API paro_status paro_quantize_activations_int8(const uint16_t* d_x, int8_t* d_q, float* d_sx, int M, int d,
+                                                    paro_dtype dtype, paro_stream_t stream);
+
+/*
+ * RMS norm with the residual's sum and int8 codes out, one pass: h = x +
+ * residual, rounded to `dtype` and stored to d_hidden (without a residual h = x;
+ * d_residual and d_hidden are given together or both NULL), then the row codes
+ * of v_c = h_c gain_c / sqrt(mean_c h_c^2 + eps), v not rounded before its codes
+ * (products h_c gain_c in fp32: exact, unless they leave fp32's range).
+ * d_gain: [d], NULL meaning ones; eps >= 0.  d_hidden may be d_x or d_residual
+ * (in place); other overlaps with outputs are refused.
+ */
+PARO_API paro_status paro_rms_norm_int8(const uint16_t* d_x, const uint16_t* d_residual, const uint16_t* d_gain,
+                                        float eps, uint16_t* d_hidden, int8_t* d_q, float* d_sx, int M, int d,
+                                        paro_dtype dtype, paro_stream_t stream);
+
+/*
+ * Build-time packing for the int8 linears: the rows of W with the transform
+ * folded in as paro_pack_weights folds it (K == 0 and d_scale == NULL: W itself),
+ * then their row codes.  d_W: fp32 [d_out][d_in], d_in % 16 == 0, d_in <= 49152;
+ * d_workspace: fp32 [d_out][d_in] with a transform, else may be NULL; d_qweight:
+ * int8 [d_out][d_in]; d_wscales: fp32 [d_out].
+ */
+PARO_API paro_status paro_pack_weights_int8(const float* d_W, int d_out, int d_in, int K, const uint16_t* d_pairs,
+                                            const float* d_cos, const float* d_sin, const float* d_scale,
+                                            float* d_workspace, int8_t* d_qweight, float* d_wscales,
+                                            paro_stream_t stream);
+
+/*
+ * int8 linear: y[m][n] = sx[m] wscales[n] sum_k q[m][k] qweight[n][k] + bias[n],
+ * the sums exact integers, the rest fp32 with one rounding to `dtype`.  d_q: int8
+ * [M][d_in], d_in % 16 == 0, d_in <= 49152; d_qweight: int8 [d_out][d_in], any
+ * d_out >= 1; codes may be any int8, -128 among them; d_bias: [d_out] or NULL;
+ * d_y: [M][d_out], overlapping no input.  No workspace.
+ */
+PARO_API paro_status paro_w8a8_linear(const int8_t* d_q, const float* d_sx, const int8_t* d_qweight,
+                                      const float* d_wscales, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in,
+                                      int d_out, paro_dtype dtype, paro_stream_t stream);
+
+/*
+ * Gated pair of int8 linears in one kernel: y = silu(g) * u with g and u the two
+ * products of paro_w8a8_linear (no bias), silu(g) = g / (1 + exp(-g)) in fp32;
+ * neither g nor u is rounded or written.  Arguments as paro_w8a8_linear.
+ */
+PARO_API paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t* d_gate_qweight,
+                                      const float* d_gate_wscales, const int8_t* d_up_qweight,
+                                      const float* d_up_wscales, uint16_t* d_y, int M, int d_in, int d_out,
+                                      paro_dtype dtype, paro_stream_t stream);
+
+/*
+ * The whole 8-bit path of one transformed linear: the activation transform (as
+ * paro_rotate, bf16 x~ into the workspace), its row codes and the int8 linear on
+ * weights of paro_pack_weights_int8, three launches on `stream`, bf16 in and out.
+ * d_workspace: paro_rotate_w8a8_workspace_bytes(M, d_in) bytes, 256-byte aligned,
+ * overlapping nothing else (x~, its codes and scales, each rounded up to 256
+ * bytes; nothing is kept there between calls).
+ */
+PARO_API size_t paro_rotate_w8a8_workspace_bytes(int M, int d_in);
+PARO_API paro_status paro_rotate_w8a8_linear(const uint16_t* d_x, int K, const uint16_t* d_pairs, const float* d_cos,
+                                             const float* d_sin, const float* d_scale, const int8_t* d_qweight,
+                                             const float* d_wscales, const uint16_t* d_bias, uint16_t* d_y, int M,
+                                             int d_in, int d_out, void* d_workspace, size_t workspace_bytes,
+                                             paro_stream_t stream);
+
+/*
  * Host-side, once per layer (no GPU involved): reorders the pairs inside every
  * stage, flipping some (i, j, cos, sin) into the same rotation (j, i, cos, -sin),
  * so that every aligned group of 32 consecutive pairs touches 32 different

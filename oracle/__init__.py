@@ -20,3 +20,4 @@ from .paro import (  # noqa: F401
 )
 from .backward import rotate_backward  # noqa: F401,E402
 from .w4a4 import dequantize_activations, quantize_activations, rotate_w4a4_linear, w4a4_linear  # noqa: F401,E402
+from .int8 import rms_norm_codes, row_codes, w8a8_linear, w8a8_swiglu  # noqa: F401,E402

@@ -21,6 +21,8 @@ __all__ = [
     "paro_batched_workspace_bytes", "paro_rotate_w4_linear_batched", "paro_plan_pair_order",
     "paro_rotate_backward_workspace_bytes", "paro_rotate_backward", "paro_set_test_hooks", "paro_dense_rotate",
     "paro_quantize_activations", "paro_w4a4_linear", "paro_rotate_w4a4_linear",
+    "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
+    "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear",
 ]
 
 # PARO_TIMELINE=1 loads the instrumented build (same kernels plus global-timer
@@ -29,7 +31,7 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)),
                         "libparo_timeline.so" if os.environ.get("PARO_TIMELINE") == "1" else "libparo.so")
 
 # name -> (restype, argtypes) of every entry point of include/paro.h
-_P, _I, _S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+_P, _I, _S, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
 EXPORTED = {
     "paro_weight_layout_version": (_I, []),
     "paro_status_string": (ctypes.c_char_p, [_I]),
@@ -52,6 +54,13 @@ EXPORTED = {
     "paro_w4a4_workspace_bytes": (_S, [_I, _I, _I, _I]),
     "paro_w4a4_linear": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _S, _P]),
     "paro_rotate_w4a4_linear": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P, _S, _P]),
+    "paro_quantize_activations_int8": (_I, [_P, _P, _P, _I, _I, _I, _P]),
+    "paro_rms_norm_int8": (_I, [_P, _P, _P, _F, _P, _P, _P, _I, _I, _I, _P]),
+    "paro_pack_weights_int8": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "paro_w8a8_linear": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "paro_w8a8_swiglu": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "paro_rotate_w8a8_workspace_bytes": (_S, [_I, _I]),
+    "paro_rotate_w8a8_linear": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _S, _P]),
 }
 
 
@@ -242,6 +251,193 @@ def paro_rotate_w4a4_linear(x: torch.Tensor, pairs, cos_t, sin_t, scale, qweight
                                      _ptr(qweight), _ptr(_u16(scales)), _ptr(_u16(zeros)), _ptr(_u16(out)), M, d_in,
                                      d_out, group_size, _ptr(workspace), workspace.numel(), _stream(stream))
     _check(st, "paro_rotate_w4a4_linear")
+    return out
+
+
+# ---- 8-bit path: the tensors' types, shapes and devices are checked here, since the
+# C ABI sees addresses only
+_ACT = {torch.bfloat16: 0, torch.float16: 1}  # paro_dtype
+
+
+def _act(dtype) -> int:
+    code = _ACT.get(dtype)
+    if code is None:
+        raise ValueError(f"expected bfloat16 or float16, got {dtype}")
+    return code
+
+
+def _rows(t: torch.Tensor, name: str):
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
+    return t.shape
+
+
+def _arg(t: torch.Tensor | None, dtype, shape, dev: int, name: str):
+    """Address of a tensor (None: NULL) after a check of its type, shape, layout and device."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name}: expected a tensor of the same CUDA device as the first one, got {t.device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous tensor")
+    return t.data_ptr()
+
+
+def _launch(fn, what: str, dev: int, stream, *args):
+    """fn(*args, stream) with `dev` current, on its current stream or the one given."""
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if st != 0:
+        _check(st, what)
+
+
+def _new(stream, shape, dtype, device):
+    """A new tensor that belongs to the stream it is first used on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def paro_quantize_activations_int8(x: torch.Tensor, *, q=None, sx=None, stream=None):
+    """Row codes of x [M, d] (bf16 or fp16): (q int8 [M, d] in -127..127, sx fp32 [M]); a code stands for q * sx."""
+    M, d = _rows(x, "x")
+    code, dev = _act(x.dtype), x.get_device()
+    px = _arg(x, x.dtype, x.shape, dev, "x")
+    if q is None:
+        q = _new(stream, (M, d), torch.int8, x.device)
+    if sx is None:
+        sx = _new(stream, (M,), torch.float32, x.device)
+    _launch(lib.paro_quantize_activations_int8, "paro_quantize_activations_int8", dev, stream, px,
+            _arg(q, torch.int8, (M, d), dev, "q"), _arg(sx, torch.float32, (M,), dev, "sx"), M, d, code)
+    return q, sx
+
+
+def paro_rms_norm_int8(x: torch.Tensor, gain=None, residual=None, *, eps: float = 1e-6, hidden=None, q=None, sx=None,
+                       stream=None):
+    """RMS norm of h = x + residual with int8 codes out; x, residual [M, d], gain [d] in bf16 or fp16.
+
+    Returns (q int8 [M, d], sx fp32 [M], hidden [M, d]); hidden is h in x's type (it may be given,
+    and may be x or residual), or None without a residual.
+    """
+    M, d = _rows(x, "x")
+    code, dev = _act(x.dtype), x.get_device()
+    if residual is None and hidden is not None:
+        raise ValueError("hidden is written only with a residual")
+    px = _arg(x, x.dtype, x.shape, dev, "x")
+    if residual is not None and hidden is None:
+        hidden = _new(stream, (M, d), x.dtype, x.device)
+    if q is None:
+        q = _new(stream, (M, d), torch.int8, x.device)
+    if sx is None:
+        sx = _new(stream, (M,), torch.float32, x.device)
+    _launch(lib.paro_rms_norm_int8, "paro_rms_norm_int8", dev, stream, px,
+            _arg(residual, x.dtype, (M, d), dev, "residual"), _arg(gain, x.dtype, (d,), dev, "gain"), eps,
+            _arg(hidden, x.dtype, (M, d), dev, "hidden"), _arg(q, torch.int8, (M, d), dev, "q"),
+            _arg(sx, torch.float32, (M,), dev, "sx"), M, d, code)
+    return q, sx, hidden
+
+
+def _tables8(pairs, cos_t, sin_t, scale, d, dev):
+    """(K, pairs, cos, sin, scale) of a transform of width d as the 8-bit calls pass it."""
+    K = _K(pairs)
+    if K and (cos_t is None or sin_t is None):
+        raise ValueError("pairs need cos_t and sin_t")
+    if pairs is not None and pairs.dtype not in (torch.int16, torch.uint16):
+        raise ValueError(f"pairs: expected int16 or uint16, got {pairs.dtype}")
+    return (K, _arg(pairs, pairs.dtype if K else None, (K, d // 2, 2), dev, "pairs") if K else None,
+            _arg(cos_t, torch.float32, (K, d // 2), dev, "cos_t") if K else None,
+            _arg(sin_t, torch.float32, (K, d // 2), dev, "sin_t") if K else None,
+            _arg(scale, torch.float32, (d,), dev, "scale"))
+
+
+def paro_pack_weights_int8(W: torch.Tensor, pairs=None, cos_t=None, sin_t=None, scale=None, *, workspace=None,
+                           qweight=None, wscales=None, stream=None):
+    """Fold the layer's transform into fp32 W [d_out, d_in] and take its row codes:
+    (qweight int8 [d_out, d_in], wscales fp32 [d_out])."""
+    d_out, d_in = _rows(W, "W")
+    dev = W.get_device()
+    pw = _arg(W, torch.float32, W.shape, dev, "W")
+    tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
+    if qweight is None:
+        qweight = _new(stream, (d_out, d_in), torch.int8, W.device)
+    if wscales is None:
+        wscales = _new(stream, (d_out,), torch.float32, W.device)
+    if tables[0] == 0 and scale is None:
+        workspace = None
+    elif workspace is None:
+        workspace = _new(stream, (d_out, d_in), torch.float32, W.device)
+    _launch(lib.paro_pack_weights_int8, "paro_pack_weights_int8", dev, stream, pw, d_out, d_in, *tables,
+            _arg(workspace, torch.float32, (d_out, d_in), dev, "workspace"),
+            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
+            _arg(wscales, torch.float32, (d_out,), dev, "wscales"))
+    return qweight, wscales
+
+
+def paro_w8a8_linear(q: torch.Tensor, sx, qweight, wscales, bias=None, *, out=None, out_dtype=torch.bfloat16,
+                     stream=None):
+    """int8 linear on codes q [M, d_in] and scales sx [M]: y = sx wscales (q qweight^T) + bias, [M, d_out] in
+    out's type or out_dtype (bf16 or fp16)."""
+    M, d_in = _rows(q, "q")
+    d_out, dev = _rows(qweight, "qweight")[0], q.get_device()
+    t = out_dtype if out is None else out.dtype
+    code = _act(t)
+    pq = _arg(q, torch.int8, q.shape, dev, "q")
+    if out is None:
+        out = _new(stream, (M, d_out), t, q.device)
+    _launch(lib.paro_w8a8_linear, "paro_w8a8_linear", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
+            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
+            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, t, (d_out,), dev, "bias"),
+            _arg(out, t, (M, d_out), dev, "out"), M, d_in, d_out, code)
+    return out
+
+
+def paro_w8a8_swiglu(q: torch.Tensor, sx, gate_qweight, gate_wscales, up_qweight, up_wscales, *, out=None,
+                     out_dtype=torch.bfloat16, stream=None):
+    """Gated pair of int8 linears in one kernel: silu(gate) * up, [M, d_out] in out's type or out_dtype."""
+    M, d_in = _rows(q, "q")
+    d_out, dev = _rows(gate_qweight, "gate_qweight")[0], q.get_device()
+    t = out_dtype if out is None else out.dtype
+    code = _act(t)
+    pq = _arg(q, torch.int8, q.shape, dev, "q")
+    if out is None:
+        out = _new(stream, (M, d_out), t, q.device)
+    _launch(lib.paro_w8a8_swiglu, "paro_w8a8_swiglu", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
+            _arg(gate_qweight, torch.int8, (d_out, d_in), dev, "gate_qweight"),
+            _arg(gate_wscales, torch.float32, (d_out,), dev, "gate_wscales"),
+            _arg(up_qweight, torch.int8, (d_out, d_in), dev, "up_qweight"),
+            _arg(up_wscales, torch.float32, (d_out,), dev, "up_wscales"), _arg(out, t, (M, d_out), dev, "out"),
+            M, d_in, d_out, code)
+    return out
+
+
+def paro_rotate_w8a8_workspace_bytes(M: int, d_in: int) -> int:
+    return int(lib.paro_rotate_w8a8_workspace_bytes(M, d_in))
+
+
+def paro_rotate_w8a8_linear(x: torch.Tensor, pairs, cos_t, sin_t, scale, qweight, wscales, bias=None, *, out=None,
+                            workspace=None, stream=None):
+    """The 8-bit path of one linear: transform, row codes, int8 linear; bf16 [M, d_in] -> bf16 [M, d_out]."""
+    M, d_in = _rows(x, "x")
+    d_out, dev = _rows(qweight, "qweight")[0], x.get_device()
+    px = _arg(x, torch.bfloat16, x.shape, dev, "x")
+    tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
+    if out is None:
+        out = _new(stream, (M, d_out), torch.bfloat16, x.device)
+    if workspace is None:
+        workspace = _new(stream, (max(paro_rotate_w8a8_workspace_bytes(M, d_in), 256),), torch.uint8, x.device)
+    _launch(lib.paro_rotate_w8a8_linear, "paro_rotate_w8a8_linear", dev, stream, px, *tables,
+            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
+            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, torch.bfloat16, (d_out,), dev, "bias"),
+            _arg(out, torch.bfloat16, (M, d_out), dev, "out"), M, d_in, d_out,
+            _arg(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
     return out
 
 

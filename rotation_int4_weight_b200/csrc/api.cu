@@ -12,6 +12,7 @@
 #include "rotate_decode.cuh"
 #include "w4_tc.cuh"
 #include "w4_stream.cuh"
+#include "int8.cuh"
 
 namespace {
 
@@ -809,6 +810,193 @@ paro_status paro_rotate_w4a4_linear(const uint16_t* d_x, int K, const uint16_t* 
   e = paro::launch_w4a4(q, sx, d_qweight, d_scales, d_zeros, d_y, M, d_in, d_out, shares > 1 ? part : nullptr,
                         shares, s);
   return from_cuda(e, "w4a4 linear launch");
+}
+
+// ---- 8-bit path ------------------------------------------------------------------------
+namespace {
+paro_status check_dtype(paro_dtype t) {
+  if (t != PARO_BF16 && t != PARO_FP16) return fail(PARO_ERR_INVALID_ARG, "unknown dtype %d", (int)t);
+  return PARO_OK;
+}
+
+paro_status check_rows(int M, int d) {
+  if (M < 0) return fail(PARO_ERR_INVALID_ARG, "M = %d is negative", M);
+  if (d <= 0) return fail(PARO_ERR_INVALID_ARG, "d = %d must be positive", d);
+  if (d > paro::kMaxDim) return fail(PARO_ERR_UNSUPPORTED, "d = %d exceeds %d", d, paro::kMaxDim);
+  return PARO_OK;
+}
+
+paro_status check_w8_shape(int d_in, int d_out) {
+  if (d_in <= 0 || d_in % 16) return fail(PARO_ERR_INVALID_ARG, "d_in = %d must be a positive multiple of 16", d_in);
+  if (d_in > paro::kMaxDim) return fail(PARO_ERR_UNSUPPORTED, "d_in = %d exceeds %d", d_in, paro::kMaxDim);
+  if (d_out <= 0) return fail(PARO_ERR_INVALID_ARG, "d_out = %d must be positive", d_out);
+  return PARO_OK;
+}
+
+paro_status check_w8_weights(const int8_t* w, const float* s) {
+  if (!w || !s) return fail(PARO_ERR_INVALID_ARG, "null weight pointer");
+  if (!aligned(w, 16) || !aligned(s, 4))
+    return fail(PARO_ERR_INVALID_ARG, "qweight must be 16-byte and wscales 4-byte aligned");
+  return PARO_OK;
+}
+
+// Checks and launches both int8 linears (d_w2 and d_s2 null: the plain one).
+paro_status run_w8a8(const int8_t* d_q, const float* d_sx, const int8_t* d_w, const float* d_s, const int8_t* d_w2,
+                     const float* d_s2, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in, int d_out,
+                     paro_dtype dtype, paro_stream_t stream) {
+  if (!d_q || !d_sx || !d_y) return fail(PARO_ERR_INVALID_ARG, "null activation pointer");
+  if (!aligned(d_q, 16) || !aligned(d_sx, 4) || !aligned(d_y, 16))
+    return fail(PARO_ERR_INVALID_ARG, "q and y must be 16-byte aligned, sx 4-byte");
+  if (d_bias && !aligned(d_bias, 2)) return fail(PARO_ERR_INVALID_ARG, "bias must be 2-byte aligned");
+  const size_t yb = (size_t)M * d_out * 2, wb = (size_t)d_out * d_in, sb = (size_t)d_out * 4;
+  if (overlap(d_y, yb, d_q, (size_t)M * d_in) || overlap(d_y, yb, d_sx, (size_t)M * 4) || overlap(d_y, yb, d_w, wb) ||
+      overlap(d_y, yb, d_s, sb) || (d_w2 && (overlap(d_y, yb, d_w2, wb) || overlap(d_y, yb, d_s2, sb))) ||
+      (d_bias && overlap(d_y, yb, d_bias, (size_t)d_out * 2)))
+    return fail(PARO_ERR_INVALID_ARG, "y overlaps an input");
+  int* status = status_ptr();
+  if (!status) return fail(PARO_ERR_CUDA, "no CUDA device / status word unavailable");
+  const paro::W8a8Args a{d_q, d_sx, d_w, d_s, d_w2, d_s2, d_bias, d_y, M, d_in, d_out, dtype == PARO_FP16};
+  return from_cuda(paro::launch_w8a8(a, status, reinterpret_cast<cudaStream_t>(stream)), "w8a8 linear launch");
+}
+}  // namespace
+
+paro_status paro_quantize_activations_int8(const uint16_t* d_x, int8_t* d_q, float* d_sx, int M, int d,
+                                           paro_dtype dtype, paro_stream_t stream) {
+  paro_status st;
+  if ((st = check_rows(M, d)) != PARO_OK || (st = check_dtype(dtype)) != PARO_OK) return st;
+  if (M == 0) return ok();
+  if (!d_x || !d_q || !d_sx) return fail(PARO_ERR_INVALID_ARG, "null pointer");
+  if (!aligned(d_x, 16) || !aligned(d_q, 16) || !aligned(d_sx, 4))
+    return fail(PARO_ERR_INVALID_ARG, "x and q must be 16-byte, sx 4-byte aligned");
+  const size_t n = (size_t)M * d, mb = (size_t)M * 4;
+  if (overlap(d_q, n, d_x, 2 * n) || overlap(d_sx, mb, d_x, 2 * n) || overlap(d_q, n, d_sx, mb))
+    return fail(PARO_ERR_INVALID_ARG, "x, q and sx must not overlap");
+  return from_cuda(paro::launch_int8_codes(d_x, nullptr, nullptr, nullptr, d_q, d_sx, M, d, dtype == PARO_FP16, false,
+                                           0.0f, reinterpret_cast<cudaStream_t>(stream)),
+                   "int8 codes launch");
+}
+
+paro_status paro_rms_norm_int8(const uint16_t* d_x, const uint16_t* d_residual, const uint16_t* d_gain, float eps,
+                               uint16_t* d_hidden, int8_t* d_q, float* d_sx, int M, int d, paro_dtype dtype,
+                               paro_stream_t stream) {
+  paro_status st;
+  if ((st = check_rows(M, d)) != PARO_OK || (st = check_dtype(dtype)) != PARO_OK) return st;
+  if (!(eps >= 0.0f) || eps > 3.0e38f) return fail(PARO_ERR_INVALID_ARG, "eps = %g must be finite and >= 0", (double)eps);
+  if (M == 0) return ok();
+  if (!d_x || !d_q || !d_sx) return fail(PARO_ERR_INVALID_ARG, "null pointer");
+  if ((d_residual != nullptr) != (d_hidden != nullptr))
+    return fail(PARO_ERR_INVALID_ARG, "residual and hidden must be given together");
+  if (!aligned(d_x, 16) || !aligned(d_q, 16) || !aligned(d_sx, 4) || !aligned(d_residual, 16) ||
+      !aligned(d_hidden, 16) || !aligned(d_gain, 16))
+    return fail(PARO_ERR_INVALID_ARG, "x, residual, gain, hidden and q must be 16-byte, sx 4-byte aligned");
+  const size_t n = (size_t)M * d, xb = 2 * n, mb = (size_t)M * 4, gb = d_gain ? (size_t)d * 2 : 0;
+  const size_t hb = d_hidden ? xb : 0;
+  if (overlap(d_q, n, d_x, xb) || overlap(d_q, n, d_residual, hb) || overlap(d_q, n, d_gain, gb) ||
+      overlap(d_q, n, d_hidden, hb) || overlap(d_q, n, d_sx, mb) || overlap(d_sx, mb, d_x, xb) ||
+      overlap(d_sx, mb, d_residual, hb) || overlap(d_sx, mb, d_gain, gb) || overlap(d_sx, mb, d_hidden, hb) ||
+      overlap(d_hidden, hb, d_gain, gb))
+    return fail(PARO_ERR_INVALID_ARG, "q, sx and hidden must overlap neither one another nor an input");
+  if ((d_hidden != d_x && overlap(d_hidden, hb, d_x, xb)) ||
+      (d_hidden != d_residual && overlap(d_hidden, hb, d_residual, hb)))
+    return fail(PARO_ERR_INVALID_ARG, "hidden partially overlaps x or the residual (only exact in-place is allowed)");
+  return from_cuda(paro::launch_int8_codes(d_x, d_residual, d_gain, d_hidden, d_q, d_sx, M, d, dtype == PARO_FP16,
+                                           true, eps, reinterpret_cast<cudaStream_t>(stream)),
+                   "rms norm launch");
+}
+
+paro_status paro_pack_weights_int8(const float* d_W, int d_out, int d_in, int K, const uint16_t* d_pairs,
+                                   const float* d_cos, const float* d_sin, const float* d_scale, float* d_workspace,
+                                   int8_t* d_qweight, float* d_wscales, paro_stream_t stream) {
+  paro_status st;
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK) return st;
+  if ((st = check_tables(K, d_in, d_pairs, d_cos, d_sin, d_scale)) != PARO_OK) return st;
+  if (!d_W || !aligned(d_W, 16)) return fail(PARO_ERR_INVALID_ARG, "W must be non-null and 16-byte aligned");
+  if ((st = check_w8_weights(d_qweight, d_wscales)) != PARO_OK) return st;
+  const bool transform = K > 0 || d_scale != nullptr;
+  const size_t n = (size_t)d_out * d_in, wb = n * sizeof(float), sb = (size_t)d_out * 4;
+  if (transform && (!d_workspace || !aligned(d_workspace, 16)))
+    return fail(PARO_ERR_INVALID_ARG, "a transform needs a 16-byte aligned fp32 [d_out][d_in] workspace");
+  if (overlap(d_qweight, n, d_W, wb) || overlap(d_wscales, sb, d_W, wb) || overlap(d_qweight, n, d_wscales, sb) ||
+      (transform && (overlap(d_workspace, wb, d_W, wb) || overlap(d_workspace, wb, d_qweight, n) ||
+                     overlap(d_workspace, wb, d_wscales, sb))))
+    return fail(PARO_ERR_INVALID_ARG, "W, workspace, qweight and wscales must not overlap");
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const float* src = d_W;
+  if (transform) {
+    int* status = status_ptr();
+    if (!status) return fail(PARO_ERR_CUDA, "no CUDA device / status word unavailable");
+    cudaError_t e = paro::launch_fold_weights(d_W, d_workspace, d_out, d_in, K, d_pairs, d_cos, d_sin, d_scale, status,
+                                              s);
+    if (e != cudaSuccess) return from_cuda(e, "fold launch");
+    src = d_workspace;
+  }
+  return from_cuda(paro::launch_int8_pack(src, d_qweight, d_wscales, d_out, d_in, s), "int8 pack launch");
+}
+
+paro_status paro_w8a8_linear(const int8_t* d_q, const float* d_sx, const int8_t* d_qweight, const float* d_wscales,
+                             const uint16_t* d_bias, uint16_t* d_y, int M, int d_in, int d_out, paro_dtype dtype,
+                             paro_stream_t stream) {
+  paro_status st;
+  if (M < 0) return fail(PARO_ERR_INVALID_ARG, "M = %d is negative", M);
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK || (st = check_dtype(dtype)) != PARO_OK) return st;
+  if (M == 0) return ok();
+  if ((st = check_w8_weights(d_qweight, d_wscales)) != PARO_OK) return st;
+  return run_w8a8(d_q, d_sx, d_qweight, d_wscales, nullptr, nullptr, d_bias, d_y, M, d_in, d_out, dtype, stream);
+}
+
+paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t* d_gate_qweight,
+                             const float* d_gate_wscales, const int8_t* d_up_qweight, const float* d_up_wscales,
+                             uint16_t* d_y, int M, int d_in, int d_out, paro_dtype dtype, paro_stream_t stream) {
+  paro_status st;
+  if (M < 0) return fail(PARO_ERR_INVALID_ARG, "M = %d is negative", M);
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK || (st = check_dtype(dtype)) != PARO_OK) return st;
+  if (M == 0) return ok();
+  if ((st = check_w8_weights(d_gate_qweight, d_gate_wscales)) != PARO_OK ||
+      (st = check_w8_weights(d_up_qweight, d_up_wscales)) != PARO_OK)
+    return st;
+  return run_w8a8(d_q, d_sx, d_gate_qweight, d_gate_wscales, d_up_qweight, d_up_wscales, nullptr, d_y, M, d_in, d_out,
+                  dtype, stream);
+}
+
+size_t paro_rotate_w8a8_workspace_bytes(int M, int d_in) {
+  if (M <= 0 || d_in <= 0) return 0;
+  return r256((size_t)M * d_in * 2) + r256((size_t)M * d_in) + r256((size_t)M * 4);
+}
+
+paro_status paro_rotate_w8a8_linear(const uint16_t* d_x, int K, const uint16_t* d_pairs, const float* d_cos,
+                                    const float* d_sin, const float* d_scale, const int8_t* d_qweight,
+                                    const float* d_wscales, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in,
+                                    int d_out, void* d_workspace, size_t workspace_bytes, paro_stream_t stream) {
+  paro_status st;
+  if (M < 0) return fail(PARO_ERR_INVALID_ARG, "M = %d is negative", M);
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK) return st;
+  if ((st = check_tables(K, d_in, d_pairs, d_cos, d_sin, d_scale)) != PARO_OK) return st;
+  if (M == 0) return ok();
+  if ((st = check_w8_weights(d_qweight, d_wscales)) != PARO_OK) return st;
+  if (!d_x || !d_y) return fail(PARO_ERR_INVALID_ARG, "null activation pointer");
+  if (!aligned(d_x, 16) || !aligned(d_y, 16)) return fail(PARO_ERR_INVALID_ARG, "x and y must be 16-byte aligned");
+  const size_t need = paro_rotate_w8a8_workspace_bytes(M, d_in);
+  if (!d_workspace || workspace_bytes < need || !aligned(d_workspace, 256))
+    return fail(PARO_ERR_INVALID_ARG, "workspace must be 256-byte aligned and hold %zu bytes", need);
+  const size_t xb = (size_t)M * d_in * 2, yb = (size_t)M * d_out * 2, wb = (size_t)d_out * d_in;
+  if (overlap(d_workspace, need, d_x, xb) || overlap(d_workspace, need, d_y, yb) ||
+      overlap(d_workspace, need, d_qweight, wb) || overlap(d_workspace, need, d_wscales, (size_t)d_out * 4) ||
+      overlap(d_y, yb, d_x, xb) || overlap(d_y, yb, d_qweight, wb) || overlap(d_y, yb, d_wscales, (size_t)d_out * 4) ||
+      (d_bias && (overlap(d_y, yb, d_bias, (size_t)d_out * 2) || overlap(d_workspace, need, d_bias, (size_t)d_out * 2))))
+    return fail(PARO_ERR_INVALID_ARG, "y, the workspace and the inputs must not overlap");
+  if (d_bias && !aligned(d_bias, 2)) return fail(PARO_ERR_INVALID_ARG, "bias must be 2-byte aligned");
+  int* status = status_ptr();
+  if (!status) return fail(PARO_ERR_CUDA, "no CUDA device / status word unavailable");
+  char* ws = static_cast<char*>(d_workspace);
+  uint16_t* xt = reinterpret_cast<uint16_t*>(ws);
+  int8_t* q = reinterpret_cast<int8_t*>(ws + r256(xb));
+  float* sx = reinterpret_cast<float*>(ws + r256(xb) + r256((size_t)M * d_in));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e = launch_transform(d_x, xt, false, M, d_in, K, d_pairs, d_cos, d_sin, d_scale, status, s, false);
+  if (e != cudaSuccess) return from_cuda(e, "rotate launch");
+  e = paro::launch_int8_codes(xt, nullptr, nullptr, nullptr, q, sx, M, d_in, false, false, 0.0f, s);
+  if (e != cudaSuccess) return from_cuda(e, "int8 codes launch");
+  return run_w8a8(q, sx, d_qweight, d_wscales, nullptr, nullptr, d_bias, d_y, M, d_in, d_out, PARO_BF16, stream);
 }
 
 paro_status paro_get_device_status(paro_stream_t stream) {

@@ -1,0 +1,29 @@
+// What follows an int8 product's 32-bit sums: scales, gate, rounding.
+#pragma once
+
+#include "int8.cuh"
+
+namespace paro {
+
+__device__ __forceinline__ float w8a8_scaled(int acc, float sx, float sw) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+}
+
+// silu(g) * u.  exp(-g) overflows to infinity for g < -88, where the quotient
+// is the right -0; fast exp and divide are within 1e-5 of g / (1 + exp(-g))
+// wherever that is not below fp32's smallest values, far inside half a step of
+// the 16-bit result (bf16 2^-9, fp16 2^-12).
+__device__ __forceinline__ float w8a8_gate(float g, float u) {
+  return __fdividef(g, 1.0f + __expf(-g)) * u;
+}
+
+template <bool F16>
+__device__ __forceinline__ float from_16(uint16_t v) {
+  return F16 ? __half2float(__ushort_as_half(v)) : __bfloat162float(__ushort_as_bfloat16(v));
+}
+template <bool F16>
+__device__ __forceinline__ uint16_t to_16(float v) {
+  return F16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+}  // namespace paro
