@@ -30,7 +30,7 @@ COMMON = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler",
 # Files whose results must be bit-exact with an IEEE reference compile without FMA contraction.
 PER_FILE = {"pack.cu": ["-fmad=false"]}
 SOURCES = ["api.cu", "rotate.cu", "rotate_decode.cu", "rotate_backward.cu", "pack.cu", "w4_gemv.cu", "w4_tc.cu", "w4_stream.cu", "plan.cu", "noalloc.cu", "w4a4.cu",
-           "int8_codes.cu", "w8a8.cu"]
+           "int8_codes.cu", "w8a8.cu", "w8a8_few.cu", "w8a8_many.cu"]
 
 
 def nvcc() -> str:

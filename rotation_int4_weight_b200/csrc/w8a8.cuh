@@ -1,9 +1,21 @@
 // What follows an int8 product's 32-bit sums: scales, gate, rounding.
 #pragma once
 
+#include <cuda.h>
+
 #include "int8.cuh"
 
 namespace paro {
+
+// The two kernels of launch_w8a8.
+cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream);
+cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream);
+
+// Tensor map of int8 [rows][d_in]: boxes of 128 columns x box_rows, 128-byte
+// swizzle, zeros outside.
+bool w8_map(CUtensorMap* map, const int8_t* p, int rows, int d_in, int box_rows);
+// Allows a kernel `bytes` of dynamic shared memory on the current device.
+cudaError_t w8_smem_limit(const void* kernel, int bytes);
 
 __device__ __forceinline__ float w8a8_scaled(int acc, float sx, float sw) {
   return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);

@@ -1,0 +1,308 @@
+// int8 linears for few tokens: weights are the tensor core's 128 rows, tokens its
+// columns, and the weights stream from HBM once.
+//
+// One CTA takes 128 output channels (with a gate, the same 128 of both weight
+// matrices), TN tokens and a share of d_in; the CTAs of a cluster hold the
+// shares of one tile:
+//   warp 0    TMA: per 128 columns of d_in the weights' 128 x 128 bytes and the
+//             tokens' TN x 128 bytes (128-byte swizzle) into a ring of stages;
+//   warp 1    MMA: four tcgen05.mma kind::i8 (128 x TN x 32) a stage, into 32-bit
+//             sums in tensor memory;
+//   warps 2-5 epilogue: thread = channel.  A cluster of one writes y from there;
+//             else every CTA lays its sums in its own shared memory (the ring is
+//             done by then), and after a cluster barrier each CTA adds up and
+//             writes its part of the tokens from all the others'.
+// Whole sums: the order of the shares does not matter, there is no workspace and
+// nothing to reset between calls.
+#include "int8.cuh"
+#include "tc_ptx.cuh"
+#include "w4_stream.cuh"  // device_sm_count
+#include "w8a8.cuh"
+
+namespace paro {
+namespace {
+
+using namespace ptx;
+
+constexpr int kRows = 128, kK = 128, kThreads = 192;
+constexpr int kMaxStages = 8;
+
+struct FewArgs {
+  CUtensorMap w, w2, q;
+  const float* sx;
+  const float* sw;
+  const float* sw2;
+  const uint16_t* bias;
+  uint16_t* y;
+  int M, d_out, blocks;  // blocks: of 128 columns of d_in
+  int split, stages;
+};
+
+template <int TN, bool GATED>
+struct FewGeo {
+  static constexpr int NW = GATED ? 2 : 1;
+  static constexpr int STAGE = NW * kRows * kK + TN * kK;
+  static constexpr int SUMS = TN * NW * kRows * 4;  // a CTA's sums for the others
+  static constexpr int COLS = NW * TN < 32 ? 32 : NW * TN;
+};
+
+template <int TN, bool GATED, bool F16>
+__global__ void __launch_bounds__(kThreads)
+w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
+  using Geo = FewGeo<TN, GATED>;
+  constexpr int NW = Geo::NW;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, s_issued, s_committed;
+
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t b_full = smem_u32(&bars[0]), b_empty = smem_u32(&bars[kMaxStages]);
+  const uint32_t b_acc = smem_u32(&bars[2 * kMaxStages]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = A.split, stages = A.stages;
+  const int rank = split > 1 ? (int)cluster_rank() : 0;
+  const int n0 = (blockIdx.x / split) * kRows, m0 = blockIdx.y * TN;
+  const int k0 = (int)((long long)rank * A.blocks / split), k1 = (int)((long long)(rank + 1) * A.blocks / split);
+  const int nk = k1 - k0;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&A.w);
+    prefetch_map(&A.q);
+    if constexpr (GATED) prefetch_map(&A.w2);
+    for (int s = 0; s < stages; ++s) {
+      mbar_init(b_full + 8 * s, 1);
+      mbar_init(b_empty + 8 * s, 1);
+    }
+    mbar_init(b_acc, 1);
+    abort_flag = 0;
+    s_issued = 0;
+    s_committed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<1>(smem_u32(&tmem_slot), Geo::COLS);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  auto fail = [&]() {
+    report_status(status, kStatusTimeout);
+    atomicExch(&abort_flag, 1);
+  };
+  auto aborted = [&]() { return *(volatile int*)&abort_flag != 0; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int i = 0;
+#pragma unroll 1
+      for (; i < nk; ++i) {
+        const int s = i % stages;
+        if (i >= stages && !mbar_wait(b_empty + 8 * s, ((i / stages) - 1) & 1)) { fail(); break; }
+        if (aborted()) break;
+        const uint32_t dst = ring + s * Geo::STAGE, bar = b_full + 8 * s;
+        const int x = (k0 + i) * kK;
+        mbar_expect_tx(bar, Geo::STAGE);
+        tma_load(dst, &A.w, x, n0, bar);
+        if constexpr (GATED) tma_load(dst + kRows * kK, &A.w2, x, n0, bar);
+        tma_load(dst + NW * kRows * kK, &A.q, x, m0, bar);
+      }
+      s_issued = i;
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      constexpr uint32_t idesc = idesc_s8(kRows, TN);
+      int i = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (; i < nk; ++i) {
+        const int s = i % stages;
+        if (!mbar_wait(b_full + 8 * s, (i / stages) & 1)) { fail(); ok = false; break; }
+        if (aborted()) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t w = ring + s * Geo::STAGE, x = w + NW * kRows * kK;
+#pragma unroll
+        for (int kk = 0; kk < kK / 32; ++kk)
+#pragma unroll
+          for (int g = 0; g < NW; ++g)
+            mma_s8<1>(tmem + g * TN, desc_sw128(w + g * kRows * kK + kk * 32), desc_sw128(x + kk * 32), idesc,
+                      (i > 0 || kk > 0) ? 1u : 0u);
+        commit(b_empty + 8 * s);
+      }
+      if (ok) commit(b_acc);
+      s_committed = i;
+    }
+  }
+  __syncwarp();
+
+  // ---- epilogue ----------------------------------------------------------------------
+  const int quarter = warp & 3, ch = quarter * 32 + lane;  // the tensor memory lanes this warp may read
+  const int n = n0 + ch;
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  const int tokens = min(TN, A.M - m0);
+  float sw[NW] = {}, bias = 0.0f;
+  bool good = true;
+  if (warp >= 2) {
+    if (n < A.d_out) {
+      sw[0] = A.sw[n];
+      if constexpr (GATED) sw[1] = A.sw2[n];
+      else if (A.bias) bias = from_16<F16>(A.bias[n]);
+    }
+    good = mbar_wait(b_acc, 0);
+    if (!good) fail();
+    tc_fence_after();
+  }
+  auto store = [&](int t, const int (&sum)[NW]) {
+    const float sx = A.sx[m0 + t];
+    float v = w8a8_scaled(sum[0], sx, sw[0]);
+    if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1], sx, sw[NW - 1]));
+    else v += bias;
+    if (n < A.d_out) A.y[(size_t)(m0 + t) * A.d_out + n] = to_16<F16>(v);
+  };
+  if (split == 1) {
+    if (warp >= 2 && good) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < tokens; c0 += 16) {
+        int v[NW][16];
+#pragma unroll
+        for (int g = 0; g < NW; ++g) tmem_ld(lanes + g * TN + c0, v[g]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (c0 + c < tokens) {
+            int sum[NW];
+#pragma unroll
+            for (int g = 0; g < NW; ++g) sum[g] = v[g][c];
+            store(c0 + c, sum);
+          }
+      }
+    }
+  } else {
+    int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
+    if (warp >= 2 && good) {
+#pragma unroll 1
+      for (int c0 = 0; c0 < tokens; c0 += 16) {
+        int v[NW][16];
+#pragma unroll
+        for (int g = 0; g < NW; ++g) tmem_ld(lanes + g * TN + c0, v[g]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          if (c0 + c < tokens)
+#pragma unroll
+            for (int g = 0; g < NW; ++g) sums[((c0 + c) * NW + g) * kRows + ch] = v[g][c];
+      }
+    }
+    // a CTA whose wait gave up has no sums: nobody of the cluster writes then
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+    if (warp >= 2) {
+      bool all = true;
+      const uint32_t flag = smem_u32(&abort_flag);
+      for (int r = 0; r < split; ++r) all &= ld_cluster(mapa(flag, r)) == 0;
+      if (all) {
+        const uint32_t mine = ring + ch * 4;
+#pragma unroll 1
+        for (int t = rank; t < tokens; t += split) {
+          int sum[NW] = {};
+#pragma unroll 1
+          for (int r = 0; r < split; ++r) {
+            const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
+#pragma unroll
+            for (int g = 0; g < NW; ++g) sum[g] += ld_cluster(at + g * kRows * 4);
+          }
+          store(t, sum);
+        }
+      }
+    }
+    __syncwarp();
+    cluster_arrive();  // the others' sums are read: their CTAs may end
+    cluster_wait();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (abort_flag && threadIdx.x == 0) {
+    // copies and MMAs in flight end before the memory goes away
+    auto last_of = [&](int cnt, int slot) { return cnt > slot ? slot + ((cnt - 1 - slot) / stages) * stages : -1; };
+    for (int s = 0; s < stages; ++s) {
+      const int jt = last_of(s_issued, s), jm = last_of(s_committed, s);
+      bool done = true;
+      if (jt >= 0) done = mbar_wait(b_full + 8 * s, (jt / stages) & 1);
+      if (jm >= 0) done = mbar_wait(b_empty + 8 * s, (jm / stages) & 1) && done;
+      if (!done) report_status(status, kStatusTimeout);
+    }
+  }
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<1>(tmem, Geo::COLS);
+  }
+}
+
+template <int TN, bool GATED, bool F16>
+cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
+  using Geo = FewGeo<TN, GATED>;
+  const int tiles = (A.d_out + kRows - 1) / kRows, mtiles = (A.M + TN - 1) / TN;
+  const int sms = device_sm_count();
+  int split = 1;
+  while (split < 8 && tiles * mtiles * split * 2 <= 2 * sms && 2 * split <= A.blocks) split *= 2;
+  A.split = split;
+  const int per = (A.blocks + split - 1) / split;
+  constexpr int kBudget = 100 * 1024;
+  int stages = kBudget / Geo::STAGE;
+  if (stages < 2) stages = 2;
+  if (stages > kMaxStages) stages = kMaxStages;
+  if (stages > per) stages = per;
+  int bytes = stages * Geo::STAGE;
+  if (split > 1 && bytes < Geo::SUMS) bytes = Geo::SUMS;
+  A.stages = stages;
+  bytes += 1024;
+  auto kernel = w8a8_few_kernel<TN, GATED, F16>;
+  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), bytes);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(tiles * split, mtiles);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = bytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, A, status);
+}
+
+template <int TN>
+cudaError_t launch_tn(const W8a8Args& a, FewArgs& A, int* status, cudaStream_t s) {
+  if (!w8_map(&A.q, a.q, a.M, a.d_in, TN)) return cudaErrorInvalidValue;
+  if (a.w2) return a.f16 ? launch_few<TN, true, true>(A, status, s) : launch_few<TN, true, false>(A, status, s);
+  return a.f16 ? launch_few<TN, false, true>(A, status, s) : launch_few<TN, false, false>(A, status, s);
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream) {
+  FewArgs A;
+  if (!w8_map(&A.w, a.w, a.d_out, a.d_in, kRows) || (a.w2 && !w8_map(&A.w2, a.w2, a.d_out, a.d_in, kRows)))
+    return cudaErrorInvalidValue;
+  A.sx = a.sx;
+  A.sw = a.sw;
+  A.sw2 = a.sw2;
+  A.bias = a.bias;
+  A.y = a.y;
+  A.M = a.M;
+  A.d_out = a.d_out;
+  A.blocks = (a.d_in + kK - 1) / kK;
+  if (a.M <= 16) return launch_tn<16>(a, A, status, stream);
+  if (a.M <= 32) return launch_tn<32>(a, A, status, stream);
+  if (a.M <= 64) return launch_tn<64>(a, A, status, stream);
+  return launch_tn<128>(a, A, status, stream);
+}
+
+}  // namespace paro

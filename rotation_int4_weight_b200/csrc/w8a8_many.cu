@@ -1,0 +1,257 @@
+// int8 linears for many tokens: pairs of CTAs on 256 x 256 tiles of the 5th-
+// generation tensor cores (tcgen05 kind::i8, cta_group::2).
+//
+// A pair (one CTA on each of two SMs) walks tiles of 256 tokens x 256 weight
+// rows; with a gate the rows are 128 of each weight matrix, so that a token's
+// gate and up sums meet in one thread.  Each CTA holds half of either operand:
+// 128 tokens and 128 weight rows (the gate's in one CTA, up's in the other), 128
+// columns of d_in a stage, and the sums of its 128 tokens in tensor memory:
+//   warp 0    TMA: its halves of a stage, completing on the first CTA's barrier;
+//   warp 1    MMA (first CTA only): four tcgen05.mma 256 x 256 x 32 a stage on
+//             both SMs, then a commit that frees the stage in both CTAs;
+//   warps 2-5 epilogue: thread = token, 32 columns at a time; scales, gate or
+//             bias, rounding, 16-byte stores.
+// Two sets of sums (2 x 256 columns of tensor memory) let the next tile's MMAs
+// run under a tile's epilogue.  Every wait is bounded.
+#include "int8.cuh"
+#include "tc_ptx.cuh"
+#include "w4_stream.cuh"  // device_sm_count
+#include "w8a8.cuh"
+
+namespace paro {
+namespace {
+
+using namespace ptx;
+
+constexpr int kTile = 256, kHalf = 128, kK = 128, kThreads = 192, kStages = 6;
+constexpr int kHalfBytes = kHalf * kK, kStageBytes = 2 * kHalfBytes;
+constexpr int kSmem = kStages * kStageBytes + 1024;
+
+struct ManyArgs {
+  CUtensorMap q, w, w2;
+  const float* sx;
+  const float* sw;
+  const float* sw2;
+  const uint16_t* bias;
+  uint16_t* y;
+  int M, d_out, blocks;  // blocks: of 128 columns of d_in
+  int mtiles, tiles;
+};
+
+template <bool GATED, bool F16>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
+  constexpr int NC = GATED ? kHalf : kTile;  // output channels of a tile
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int abort_flag, s_issued, s_committed;
+
+  unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t ring = smem_u32(smem);
+  const uint32_t b_full = smem_u32(&bars[0]), b_empty = smem_u32(&bars[kStages]);
+  const uint32_t b_acc_full = smem_u32(&bars[2 * kStages]), b_acc_empty = smem_u32(&bars[2 * kStages + 2]);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (warp == 0 && lane == 0) {
+    prefetch_map(&A.q);
+    prefetch_map(GATED && rank ? &A.w2 : &A.w);
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(b_full + 8 * s, 1);   // (first CTA) its own arrival and both CTAs' bytes
+      mbar_init(b_empty + 8 * s, 1);  // the commit of the MMAs that read the stage
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(b_acc_full + 8 * s, 1);
+      mbar_init(b_acc_empty + 8 * s, 8);  // (first CTA) the epilogue warps of both CTAs
+    }
+    abort_flag = 0;
+    s_issued = 0;
+    s_committed = 0;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<2>(smem_u32(&tmem_slot), 512);
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // the other CTA's barriers and tensor memory are ready
+  cluster_wait();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+
+  auto fail = [&]() {
+    report_status(status, kStatusTimeout);
+    atomicExch(&abort_flag, 1);
+  };
+  auto aborted = [&]() { return *(volatile int*)&abort_flag != 0; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      const CUtensorMap* wmap = GATED && rank ? &A.w2 : &A.w;
+      int it = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int t = pair; ok && t < A.tiles; t += pairs) {
+        const int m0 = (t % A.mtiles) * kTile + rank * kHalf;
+        const int n0 = (t / A.mtiles) * NC + (GATED ? 0 : rank * kHalf);
+#pragma unroll 1
+        for (int k = 0; k < A.blocks; ++k, ++it) {
+          const int s = it % kStages;
+          if (it >= kStages && !mbar_wait(b_empty + 8 * s, ((it / kStages) - 1) & 1)) { fail(); ok = false; break; }
+          if (aborted()) { ok = false; break; }
+          const uint32_t bar = mapa(b_full + 8 * s, 0), dst = ring + s * kStageBytes;
+          if (rank == 0) mbar_expect_tx(b_full + 8 * s, 2 * kStageBytes);
+          tma_load_pair(dst, &A.q, k * kK, m0, bar);
+          tma_load_pair(dst + kHalfBytes, wmap, k * kK, n0, bar);
+        }
+      }
+      s_issued = it;
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      constexpr uint32_t idesc = idesc_s8(kTile, kTile);
+      int it = 0, j = 0;
+      bool ok = true;
+#pragma unroll 1
+      for (int t = pair; ok && t < A.tiles; t += pairs, ++j) {
+        const int acc = j & 1;
+        if (j >= 2 && !mbar_wait(b_acc_empty + 8 * acc, ((j >> 1) - 1) & 1)) { fail(); break; }
+        tc_fence_after();
+#pragma unroll 1
+        for (int k = 0; k < A.blocks; ++k, ++it) {
+          const int s = it % kStages;
+          if (!mbar_wait(b_full + 8 * s, (it / kStages) & 1)) { fail(); ok = false; break; }
+          if (aborted()) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t a = ring + s * kStageBytes, b = a + kHalfBytes;
+#pragma unroll
+          for (int kk = 0; kk < kK / 32; ++kk)
+            mma_s8<2>(tmem + acc * kTile, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc,
+                      (k > 0 || kk > 0) ? 1u : 0u);
+          commit_pair(b_empty + 8 * s);
+        }
+        if (ok) commit_pair(b_acc_full + 8 * acc);
+      }
+      s_committed = it;
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+    int j = 0;
+#pragma unroll 1
+    for (int t = pair; t < A.tiles; t += pairs, ++j) {
+      const int acc = j & 1;
+      const int m = (t % A.mtiles) * kTile + rank * kHalf + quarter * 32 + lane, n0 = (t / A.mtiles) * NC;
+      const float sx = m < A.M ? A.sx[m] : 0.0f;
+      if (!mbar_wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
+      tc_fence_after();
+#pragma unroll 1
+      for (int c0 = 0; c0 < NC && n0 + c0 < A.d_out; c0 += 32) {
+        int v[32], u[GATED ? 32 : 1];
+        tmem_ld(lanes + acc * kTile + c0, v);
+        if constexpr (GATED) tmem_ld(lanes + acc * kTile + kHalf + c0, u);
+        tmem_ld_wait();
+        if (m >= A.M) continue;
+        const int n = n0 + c0;
+        uint16_t* dst = A.y + (size_t)m * A.d_out + n;
+        const bool whole = n + 32 <= A.d_out;
+        uint32_t o[16];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          float f = 0.0f;
+          if (whole || n + c < A.d_out) {
+            f = w8a8_scaled(v[c], sx, __ldg(A.sw + n + c));
+            if constexpr (GATED) f = w8a8_gate(f, w8a8_scaled(u[c], sx, __ldg(A.sw2 + n + c)));
+            else if (A.bias) f += from_16<F16>(__ldg(A.bias + n + c));
+          }
+          const uint32_t h = to_16<F16>(f);
+          if (c & 1) o[c >> 1] |= h << 16;
+          else o[c >> 1] = h;
+        }
+        if (whole && (A.d_out & 7) == 0) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < 32; ++c)
+            if (n + c < A.d_out) dst[c] = (uint16_t)(o[c >> 1] >> (16 * (c & 1)));
+        }
+      }
+      __syncwarp();
+      tc_fence_before();
+      if (lane == 0) mbar_arrive_cluster(mapa(b_acc_empty + 8 * acc, 0));
+    }
+  }
+
+  // ---- teardown ----------------------------------------------------------------------
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_arrive();  // both CTAs are done with the other's barriers and shared memory, unless a wait gave up:
+  cluster_wait();
+  bool any = abort_flag != 0;
+  any |= ld_cluster(mapa(smem_u32(&abort_flag), rank ^ 1)) != 0;
+  if (any) {
+    // then copies and MMAs in flight end before the memory goes away.  The two
+    // CTAs may have issued different numbers of stages: a slot's last phase is
+    // made whole by what the one that stopped first did not send
+    if (rank == 0 && threadIdx.x == 0) {
+      const int mine = s_issued, theirs = ld_cluster(mapa(smem_u32(&s_issued), 1));
+      auto last_of = [](int cnt, int slot) { return cnt > slot ? slot + ((cnt - 1 - slot) / kStages) * kStages : -1; };
+      bool done = true;
+      for (int s = 0; s < kStages; ++s) {
+        const int a = last_of(mine, s), b = last_of(theirs, s), jm = last_of(s_committed, s);
+        if (a > b) mbar_complete_tx(b_full + 8 * s, kStageBytes);
+        if (b > a) mbar_expect_tx(b_full + 8 * s, kStageBytes);
+        const int last = a > b ? a : b;
+        if (last >= 0) done = mbar_wait(b_full + 8 * s, (last / kStages) & 1) && done;
+        if (jm >= 0) done = mbar_wait(b_empty + 8 * s, (jm / kStages) & 1) && done;
+      }
+      if (!done) report_status(status, kStatusTimeout);
+    }
+    __syncthreads();
+    cluster_arrive();
+    cluster_wait();
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc<2>(tmem, 512);
+  }
+  cluster_arrive();  // neither CTA ends while the other may still read it
+  cluster_wait();
+}
+
+template <bool GATED, bool F16>
+cudaError_t launch_many(const ManyArgs& A, int* status, cudaStream_t s) {
+  auto kernel = w8a8_many_kernel<GATED, F16>;
+  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kSmem);
+  if (e != cudaSuccess) return e;
+  const int pairs = device_sm_count() / 2;
+  kernel<<<2 * (A.tiles < pairs ? A.tiles : pairs), kThreads, kSmem, s>>>(A, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream) {
+  ManyArgs A;
+  if (!w8_map(&A.q, a.q, a.M, a.d_in, kHalf) || !w8_map(&A.w, a.w, a.d_out, a.d_in, kHalf) ||
+      (a.w2 && !w8_map(&A.w2, a.w2, a.d_out, a.d_in, kHalf)))
+    return cudaErrorInvalidValue;
+  A.sx = a.sx;
+  A.sw = a.sw;
+  A.sw2 = a.sw2;
+  A.bias = a.bias;
+  A.y = a.y;
+  A.M = a.M;
+  A.d_out = a.d_out;
+  A.blocks = (a.d_in + kK - 1) / kK;
+  A.mtiles = (a.M + kTile - 1) / kTile;
+  const int nc = a.w2 ? kHalf : kTile;
+  A.tiles = A.mtiles * ((a.d_out + nc - 1) / nc);
+  if (a.w2) return a.f16 ? launch_many<true, true>(A, status, stream) : launch_many<true, false>(A, status, stream);
+  return a.f16 ? launch_many<false, true>(A, status, stream) : launch_many<false, false>(A, status, stream);
+}
+
+}  // namespace paro
