@@ -25,7 +25,7 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128, kK = 128, kThreads = 192;
-constexpr int kMaxStages = 8;
+constexpr int kMaxStages = 8, kMaxSplit = 8;  // 8: the portable size of a cluster
 
 struct FewArgs {
   CUtensorMap w, w2, q;
@@ -55,6 +55,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, s_issued, s_committed;
+  __shared__ float s_sx[TN];
 
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_u32(smem);
@@ -144,6 +145,8 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   float sw[NW] = {}, bias = 0.0f;
   bool good = true;
   if (warp >= 2) {
+    for (int t = threadIdx.x - 64; t < tokens; t += kRows) s_sx[t] = A.sx[m0 + t];
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");
     if (n < A.d_out) {
       sw[0] = A.sw[n];
       if constexpr (GATED) sw[1] = A.sw2[n];
@@ -154,7 +157,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     tc_fence_after();
   }
   auto store = [&](int t, const int (&sum)[NW]) {
-    const float sx = A.sx[m0 + t];
+    const float sx = s_sx[t];
     float v = w8a8_scaled(sum[0], sx, sw[0]);
     if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1], sx, sw[NW - 1]));
     else v += bias;
@@ -199,20 +202,27 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     cluster_arrive();
     cluster_wait();
     if (warp >= 2) {
-      bool all = true;
       const uint32_t flag = smem_u32(&abort_flag);
-      for (int r = 0; r < split; ++r) all &= ld_cluster(mapa(flag, r)) == 0;
+      const bool all = __all_sync(0xffffffffu, lane >= split || ld_cluster(mapa(flag, lane)) == 0);
       if (all) {
         const uint32_t mine = ring + ch * 4;
 #pragma unroll 1
         for (int t = rank; t < tokens; t += split) {
           int sum[NW] = {};
-#pragma unroll 1
-          for (int r = 0; r < split; ++r) {
-            const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
+          // all the loads, then their sum: their latency is paid once
+          int part[NW][kMaxSplit];
 #pragma unroll
-            for (int g = 0; g < NW; ++g) sum[g] += ld_cluster(at + g * kRows * 4);
-          }
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < split) {
+              const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
+#pragma unroll
+              for (int g = 0; g < NW; ++g) part[g][r] = ld_cluster(at + g * kRows * 4);
+            }
+#pragma unroll
+          for (int r = 0; r < kMaxSplit; ++r)
+            if (r < split)
+#pragma unroll
+              for (int g = 0; g < NW; ++g) sum[g] += part[g][r];
           store(t, sum);
         }
       }
@@ -248,7 +258,7 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
   const int tiles = (A.d_out + kRows - 1) / kRows, mtiles = (A.M + TN - 1) / TN;
   const int sms = device_sm_count();
   int split = 1;
-  while (split < 8 && tiles * mtiles * split * 2 <= 2 * sms && 2 * split <= A.blocks) split *= 2;
+  while (split < kMaxSplit && tiles * mtiles * split * 2 <= 2 * sms && 2 * split <= A.blocks) split *= 2;
   A.split = split;
   const int per = (A.blocks + split - 1) / split;
   constexpr int kBudget = 100 * 1024;

@@ -46,6 +46,8 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
   __shared__ __align__(8) uint64_t bars[2 * kStages + 4];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, s_issued, s_committed;
+  // a tile's channel scales, with the up scales behind the gate's, and its bias
+  __shared__ __align__(16) float s_sw[2][kTile], s_bias[2][GATED ? 4 : kTile];
 
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_u32(smem);
@@ -143,6 +145,15 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       const int acc = j & 1;
       const int m = (t % A.mtiles) * kTile + rank * kHalf + quarter * 32 + lane, n0 = (t / A.mtiles) * NC;
       const float sx = m < A.M ? A.sx[m] : 0.0f;
+      // the tile's channel values, while its MMAs run; two sets, so that a warp
+      // may be one tile ahead of another
+      for (int c = threadIdx.x - 64; c < kTile; c += 128) {
+        const bool up = GATED && c >= kHalf;
+        const int n = n0 + (up ? c - kHalf : c);
+        s_sw[acc][c] = n < A.d_out ? (up ? A.sw2 : A.sw)[n] : 0.0f;
+        if constexpr (!GATED) s_bias[acc][c] = A.bias && n < A.d_out ? from_16<F16>(A.bias[n]) : 0.0f;
+      }
+      asm volatile("bar.sync 1, 128;\n" ::: "memory");
       if (!mbar_wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
       tc_fence_after();
 #pragma unroll 1
@@ -154,21 +165,26 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         if (m >= A.M) continue;
         const int n = n0 + c0;
         uint16_t* dst = A.y + (size_t)m * A.d_out + n;
-        const bool whole = n + 32 <= A.d_out;
         uint32_t o[16];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          float f = 0.0f;
-          if (whole || n + c < A.d_out) {
-            f = w8a8_scaled(v[c], sx, __ldg(A.sw + n + c));
-            if constexpr (GATED) f = w8a8_gate(f, w8a8_scaled(u[c], sx, __ldg(A.sw2 + n + c)));
-            else if (A.bias) f += from_16<F16>(__ldg(A.bias + n + c));
+        for (int c = 0; c < 32; c += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(&s_sw[acc][c0 + c]);
+          float f[4] = {w8a8_scaled(v[c], sx, w.x), w8a8_scaled(v[c + 1], sx, w.y), w8a8_scaled(v[c + 2], sx, w.z),
+                        w8a8_scaled(v[c + 3], sx, w.w)};
+          if constexpr (GATED) {
+            const float4 w2 = *reinterpret_cast<const float4*>(&s_sw[acc][kHalf + c0 + c]);
+            f[0] = w8a8_gate(f[0], w8a8_scaled(u[c], sx, w2.x));
+            f[1] = w8a8_gate(f[1], w8a8_scaled(u[c + 1], sx, w2.y));
+            f[2] = w8a8_gate(f[2], w8a8_scaled(u[c + 2], sx, w2.z));
+            f[3] = w8a8_gate(f[3], w8a8_scaled(u[c + 3], sx, w2.w));
+          } else {
+            const float4 b = *reinterpret_cast<const float4*>(&s_bias[acc][c0 + c]);
+            f[0] += b.x, f[1] += b.y, f[2] += b.z, f[3] += b.w;
           }
-          const uint32_t h = to_16<F16>(f);
-          if (c & 1) o[c >> 1] |= h << 16;
-          else o[c >> 1] = h;
+          o[c / 2] = to_16<F16>(f[0]) | ((uint32_t)to_16<F16>(f[1]) << 16);
+          o[c / 2 + 1] = to_16<F16>(f[2]) | ((uint32_t)to_16<F16>(f[3]) << 16);
         }
-        if (whole && (A.d_out & 7) == 0) {
+        if (n + 32 <= A.d_out && (A.d_out & 7) == 0) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
