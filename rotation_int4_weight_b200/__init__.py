@@ -287,36 +287,44 @@ def _arg(t: torch.Tensor | None, dtype, shape, dev: int, name: str):
 
 def _launch(fn, what: str, dev: int, stream, *args):
     """fn(*args, stream) with `dev` current, on its current stream or the one given."""
-    if stream is not None and stream.device.index != dev:
+    if stream is None:
+        handle = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device.index == dev:
+        handle = stream.cuda_stream
+    else:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
-    if torch.cuda.current_device() == dev:
-        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+    if torch._C._cuda_getDevice() == dev:
+        st = fn(*args, handle)
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
+            st = fn(*args, handle)
     if st != 0:
         _check(st, what)
 
 
-def _new(stream, shape, dtype, device):
+def _new(stream, dtype, device, *shape):
     """A new tensor that belongs to the stream it is first used on."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return torch.empty(*shape, dtype=dtype, device=device)
 
 
 def paro_quantize_activations_int8(x: torch.Tensor, *, q=None, sx=None, stream=None):
     """Row codes of x [M, d] (bf16 or fp16): (q int8 [M, d] in -127..127, sx fp32 [M]); a code stands for q * sx."""
     M, d = _rows(x, "x")
-    code, dev = _act(x.dtype), x.get_device()
-    px = _arg(x, x.dtype, x.shape, dev, "x")
+    t, dev = x.dtype, x.get_device()
+    code, px = _act(t), _arg(x, t, x.shape, dev, "x")
     if q is None:
-        q = _new(stream, (M, d), torch.int8, x.device)
+        q = _new(stream, torch.int8, x.device, M, d)
+    else:
+        _arg(q, torch.int8, (M, d), dev, "q")
     if sx is None:
-        sx = _new(stream, (M,), torch.float32, x.device)
-    _launch(lib.paro_quantize_activations_int8, "paro_quantize_activations_int8", dev, stream, px,
-            _arg(q, torch.int8, (M, d), dev, "q"), _arg(sx, torch.float32, (M,), dev, "sx"), M, d, code)
+        sx = _new(stream, torch.float32, x.device, M)
+    else:
+        _arg(sx, torch.float32, (M,), dev, "sx")
+    _launch(lib.paro_quantize_activations_int8, "paro_quantize_activations_int8", dev, stream, px, q.data_ptr(),
+            sx.data_ptr(), M, d, code)
     return q, sx
 
 
@@ -328,20 +336,26 @@ def paro_rms_norm_int8(x: torch.Tensor, gain=None, residual=None, *, eps: float 
     and may be x or residual), or None without a residual.
     """
     M, d = _rows(x, "x")
-    code, dev = _act(x.dtype), x.get_device()
     if residual is None and hidden is not None:
         raise ValueError("hidden is written only with a residual")
-    px = _arg(x, x.dtype, x.shape, dev, "x")
-    if residual is not None and hidden is None:
-        hidden = _new(stream, (M, d), x.dtype, x.device)
+    t, dev = x.dtype, x.get_device()
+    code, px = _act(t), _arg(x, t, x.shape, dev, "x")
+    pr, pg = _arg(residual, t, x.shape, dev, "residual"), _arg(gain, t, (d,), dev, "gain")
+    if residual is not None:
+        if hidden is None:
+            hidden = _new(stream, t, x.device, M, d)
+        else:
+            _arg(hidden, t, x.shape, dev, "hidden")
     if q is None:
-        q = _new(stream, (M, d), torch.int8, x.device)
+        q = _new(stream, torch.int8, x.device, M, d)
+    else:
+        _arg(q, torch.int8, (M, d), dev, "q")
     if sx is None:
-        sx = _new(stream, (M,), torch.float32, x.device)
-    _launch(lib.paro_rms_norm_int8, "paro_rms_norm_int8", dev, stream, px,
-            _arg(residual, x.dtype, (M, d), dev, "residual"), _arg(gain, x.dtype, (d,), dev, "gain"), eps,
-            _arg(hidden, x.dtype, (M, d), dev, "hidden"), _arg(q, torch.int8, (M, d), dev, "q"),
-            _arg(sx, torch.float32, (M,), dev, "sx"), M, d, code)
+        sx = _new(stream, torch.float32, x.device, M)
+    else:
+        _arg(sx, torch.float32, (M,), dev, "sx")
+    _launch(lib.paro_rms_norm_int8, "paro_rms_norm_int8", dev, stream, px, pr, pg, eps,
+            None if hidden is None else hidden.data_ptr(), q.data_ptr(), sx.data_ptr(), M, d, code)
     return q, sx, hidden
 
 
@@ -367,13 +381,13 @@ def paro_pack_weights_int8(W: torch.Tensor, pairs=None, cos_t=None, sin_t=None, 
     pw = _arg(W, torch.float32, W.shape, dev, "W")
     tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
     if qweight is None:
-        qweight = _new(stream, (d_out, d_in), torch.int8, W.device)
+        qweight = _new(stream, torch.int8, W.device, d_out, d_in)
     if wscales is None:
-        wscales = _new(stream, (d_out,), torch.float32, W.device)
+        wscales = _new(stream, torch.float32, W.device, d_out)
     if tables[0] == 0 and scale is None:
         workspace = None
     elif workspace is None:
-        workspace = _new(stream, (d_out, d_in), torch.float32, W.device)
+        workspace = _new(stream, torch.float32, W.device, d_out, d_in)
     _launch(lib.paro_pack_weights_int8, "paro_pack_weights_int8", dev, stream, pw, d_out, d_in, *tables,
             _arg(workspace, torch.float32, (d_out, d_in), dev, "workspace"),
             _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
@@ -391,11 +405,13 @@ def paro_w8a8_linear(q: torch.Tensor, sx, qweight, wscales, bias=None, *, out=No
     code = _act(t)
     pq = _arg(q, torch.int8, q.shape, dev, "q")
     if out is None:
-        out = _new(stream, (M, d_out), t, q.device)
+        out = _new(stream, t, q.device, M, d_out)
+    else:
+        _arg(out, t, (M, d_out), dev, "out")
     _launch(lib.paro_w8a8_linear, "paro_w8a8_linear", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
             _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
-            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, t, (d_out,), dev, "bias"),
-            _arg(out, t, (M, d_out), dev, "out"), M, d_in, d_out, code)
+            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, t, (d_out,), dev, "bias"), out.data_ptr(),
+            M, d_in, d_out, code)
     return out
 
 
@@ -408,13 +424,14 @@ def paro_w8a8_swiglu(q: torch.Tensor, sx, gate_qweight, gate_wscales, up_qweight
     code = _act(t)
     pq = _arg(q, torch.int8, q.shape, dev, "q")
     if out is None:
-        out = _new(stream, (M, d_out), t, q.device)
+        out = _new(stream, t, q.device, M, d_out)
+    else:
+        _arg(out, t, (M, d_out), dev, "out")
     _launch(lib.paro_w8a8_swiglu, "paro_w8a8_swiglu", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
             _arg(gate_qweight, torch.int8, (d_out, d_in), dev, "gate_qweight"),
             _arg(gate_wscales, torch.float32, (d_out,), dev, "gate_wscales"),
             _arg(up_qweight, torch.int8, (d_out, d_in), dev, "up_qweight"),
-            _arg(up_wscales, torch.float32, (d_out,), dev, "up_wscales"), _arg(out, t, (M, d_out), dev, "out"),
-            M, d_in, d_out, code)
+            _arg(up_wscales, torch.float32, (d_out,), dev, "up_wscales"), out.data_ptr(), M, d_in, d_out, code)
     return out
 
 
@@ -430,9 +447,9 @@ def paro_rotate_w8a8_linear(x: torch.Tensor, pairs, cos_t, sin_t, scale, qweight
     px = _arg(x, torch.bfloat16, x.shape, dev, "x")
     tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
     if out is None:
-        out = _new(stream, (M, d_out), torch.bfloat16, x.device)
+        out = _new(stream, torch.bfloat16, x.device, M, d_out)
     if workspace is None:
-        workspace = _new(stream, (max(paro_rotate_w8a8_workspace_bytes(M, d_in), 256),), torch.uint8, x.device)
+        workspace = _new(stream, torch.uint8, x.device, max(paro_rotate_w8a8_workspace_bytes(M, d_in), 256))
     _launch(lib.paro_rotate_w8a8_linear, "paro_rotate_w8a8_linear", dev, stream, px, *tables,
             _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
             _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, torch.bfloat16, (d_out,), dev, "bias"),

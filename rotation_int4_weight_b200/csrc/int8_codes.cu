@@ -25,6 +25,7 @@
 // last chunk of such a row go value by value, and its gain comes from two
 // aligned 16-byte loads shifted by the row's phase.
 #include "int8.cuh"
+#include "tc_ptx.cuh"
 
 namespace paro {
 namespace {
@@ -153,6 +154,8 @@ __global__ void __launch_bounds__(1024)
 codes_kernel(const CodeArgs A) {
   __shared__ uint32_t red_a[32];
   __shared__ float red_s[32];
+  ptx::grid_trigger();
+  ptx::grid_wait();  // launched over the end of the kernel before; nothing is read or written until that is done
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= A.M) return;  // whole warps: a CTA of several rows has one warp for each and no barrier
   const int d = A.d, T1 = blockDim.x;
@@ -300,12 +303,19 @@ codes_kernel(const CodeArgs A) {
 template <typename T, bool NORM, bool EVEN>
 cudaError_t launch_nc(const CodeArgs& A, int nc, int threads, cudaStream_t s) {
   const int rows = threads == 32 ? 4 : 1;
-  const dim3 block(threads, rows), grid((unsigned)((A.M + rows - 1) / rows));
-  if (nc <= 1) codes_kernel<T, 1, NORM, EVEN><<<grid, block, 0, s>>>(A);
-  else if (nc <= 2) codes_kernel<T, 2, NORM, EVEN><<<grid, block, 0, s>>>(A);
-  else if (nc <= 4) codes_kernel<T, 4, NORM, EVEN><<<grid, block, 0, s>>>(A);
-  else codes_kernel<T, 8, NORM, EVEN><<<grid, block, 0, s>>>(A);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((A.M + rows - 1) / rows));
+  cfg.blockDim = dim3(threads, rows);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (nc <= 1) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 1, NORM, EVEN>, A);
+  if (nc <= 2) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 2, NORM, EVEN>, A);
+  if (nc <= 4) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 4, NORM, EVEN>, A);
+  return cudaLaunchKernelEx(&cfg, codes_kernel<T, 8, NORM, EVEN>, A);
 }
 
 template <typename T, bool NORM>

@@ -5,6 +5,7 @@
 // exact 32-bit integers (|sum| <= 49152 * 2^14 < 2^31), so they do not depend on
 // any order; what follows is fp32 and one rounding to y's type.
 #include <atomic>
+#include <cstdlib>
 
 #include "int8.cuh"
 #include "w8a8.cuh"
@@ -42,12 +43,28 @@ bool w8_map(CUtensorMap* map, const int8_t* p, int rows, int d_in, int box_rows)
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t w8_smem_limit(const void* kernel, int bytes) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+bool w8_out_map(CUtensorMap* map, const uint16_t* y, int rows, int d_out) {
+  const EncodeTiled enc = encode_fn();
+  const cuuint64_t dims[2] = {(cuuint64_t)d_out, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)d_out * 2};
+  const cuuint32_t box[2] = {32, 32}, elem[2] = {1, 1};
+  return enc && enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<uint16_t*>(y), dims, strides, box, elem,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+cudaError_t w8_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
 }
 
 cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream) {
-  if (a.M <= 128) return launch_w8a8_few(a, status, stream);
+  if (getenv("W8F") ? a.M <= atoi(getenv("W8F")) : a.M <= 128) return launch_w8a8_few(a, status, stream);
   return launch_w8a8_many(a, status, stream);
 }
 

@@ -8,12 +8,16 @@
 //             tokens' TN x 128 bytes (128-byte swizzle) into a ring of stages;
 //   warp 1    MMA: four tcgen05.mma kind::i8 (128 x TN x 32) a stage, into 32-bit
 //             sums in tensor memory;
-//   warps 2-5 epilogue: thread = channel.  A cluster of one writes y from there;
-//             else every CTA lays its sums in its own shared memory (the ring is
+//   warps 2-5 epilogue: the sums go to the CTA's own shared memory (the ring is
 //             done by then), and after a cluster barrier each CTA adds up and
-//             writes its part of the tokens from all the others'.
+//             writes its part of the tokens from all the others': a warp takes a
+//             token, a lane four channels, the loads of all shares at once.
 // Whole sums: the order of the shares does not matter, there is no workspace and
 // nothing to reset between calls.
+//
+// The launch overlaps the kernel before it: until that one is done a CTA sets up
+// its barriers and asks for its weights in L2 only, which is right whoever wrote
+// them last; every read and write of its own comes after the wait.
 #include "int8.cuh"
 #include "tc_ptx.cuh"
 #include "w4_stream.cuh"  // device_sm_count
@@ -25,7 +29,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128, kK = 128, kThreads = 192;
+constexpr int kMaxSmem = 130 * 1024;  // a CTA's ring, or its sums for 128 tokens of a gated pair
 constexpr int kMaxStages = 8, kMaxSplit = 8;  // 8: the portable size of a cluster
+constexpr int kAhead = 32;  // stages asked for in L2 before the kernel before is done
 
 struct FewArgs {
   CUtensorMap w, w2, q;
@@ -87,6 +93,14 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  grid_trigger();
+  if (warp == 0 && lane == 0) {
+    for (int i = 0; i < nk && i < kAhead; ++i) {
+      tma_prefetch(&A.w, (k0 + i) * kK, n0);
+      if constexpr (GATED) tma_prefetch(&A.w2, (k0 + i) * kK, n0);
+    }
+  }
+  grid_wait();
 
   auto fail = [&]() {
     report_status(status, kStatusTimeout);
@@ -138,52 +152,23 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   __syncwarp();
 
   // ---- epilogue ----------------------------------------------------------------------
-  const int quarter = warp & 3, ch = quarter * 32 + lane;  // the tensor memory lanes this warp may read
-  const int n = n0 + ch;
-  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
   const int tokens = min(TN, A.M - m0);
-  float sw[NW] = {}, bias = 0.0f;
-  bool good = true;
+  const int n = n0 + 4 * lane;  // this lane's channels n .. n + 3, of warp - 2, warp + 2, ...'s tokens
+  float sw[NW][4], bias[4];
   if (warp >= 2) {
     for (int t = threadIdx.x - 64; t < tokens; t += kRows) s_sx[t] = A.sx[m0 + t];
-    asm volatile("bar.sync 1, 128;\n" ::: "memory");
-    if (n < A.d_out) {
-      sw[0] = A.sw[n];
-      if constexpr (GATED) sw[1] = A.sw2[n];
-      else if (A.bias) bias = from_16<F16>(A.bias[n]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const bool in = n + e < A.d_out;
+      sw[0][e] = in ? A.sw[n + e] : 0.0f;
+      if constexpr (GATED) sw[NW - 1][e] = in ? A.sw2[n + e] : 0.0f;
+      bias[e] = !GATED && A.bias && in ? from_16<F16>(A.bias[n + e]) : 0.0f;
     }
-    good = mbar_wait(b_acc, 0);
-    if (!good) fail();
-    tc_fence_after();
-  }
-  auto store = [&](int t, const int (&sum)[NW]) {
-    const float sx = s_sx[t];
-    float v = w8a8_scaled(sum[0], sx, sw[0]);
-    if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1], sx, sw[NW - 1]));
-    else v += bias;
-    if (n < A.d_out) A.y[(size_t)(m0 + t) * A.d_out + n] = to_16<F16>(v);
-  };
-  if (split == 1) {
-    if (warp >= 2 && good) {
-#pragma unroll 1
-      for (int c0 = 0; c0 < tokens; c0 += 16) {
-        int v[NW][16];
-#pragma unroll
-        for (int g = 0; g < NW; ++g) tmem_ld(lanes + g * TN + c0, v[g]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < tokens) {
-            int sum[NW];
-#pragma unroll
-            for (int g = 0; g < NW; ++g) sum[g] = v[g][c];
-            store(c0 + c, sum);
-          }
-      }
-    }
-  } else {
-    int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
-    if (warp >= 2 && good) {
+    if (mbar_wait(b_acc, 0)) {
+      tc_fence_after();
+      const int quarter = warp & 3, ch = quarter * 32 + lane;  // the tensor memory lanes this warp may read
+      const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+      int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
 #pragma unroll 1
       for (int c0 = 0; c0 < tokens; c0 += 16) {
         int v[NW][16];
@@ -196,38 +181,66 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
 #pragma unroll
             for (int g = 0; g < NW; ++g) sums[((c0 + c) * NW + g) * kRows + ch] = v[g][c];
       }
+    } else {
+      fail();
     }
-    // a CTA whose wait gave up has no sums: nobody of the cluster writes then
-    __syncwarp();
+  }
+  // the sums of all shares are there; a CTA whose wait gave up has none, and
+  // nobody of its cluster writes then
+  __syncwarp();
+  if (split > 1) {
     cluster_arrive();
     cluster_wait();
-    if (warp >= 2) {
-      const uint32_t flag = smem_u32(&abort_flag);
-      const bool all = __all_sync(0xffffffffu, lane >= split || ld_cluster(mapa(flag, lane)) == 0);
-      if (all) {
-        const uint32_t mine = ring + ch * 4;
-#pragma unroll 1
-        for (int t = rank; t < tokens; t += split) {
-          int sum[NW] = {};
-          // all the loads, then their sum: their latency is paid once
-          int part[NW][kMaxSplit];
+  } else {
+    __syncthreads();
+  }
+  if (warp >= 2) {
+    const uint32_t flag = smem_u32(&abort_flag);
+    if (__all_sync(0xffffffffu, lane >= split || ld_cluster(mapa(flag, lane)) == 0)) {
+      const uint32_t mine = ring + lane * 16;
+#pragma unroll 2
+      for (int t = rank + split * (warp - 2); t < tokens; t += split * 4) {
+        int4 part[NW][kMaxSplit];
 #pragma unroll
-          for (int r = 0; r < kMaxSplit; ++r)
-            if (r < split) {
-              const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split) {
+            const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
 #pragma unroll
-              for (int g = 0; g < NW; ++g) part[g][r] = ld_cluster(at + g * kRows * 4);
+            for (int g = 0; g < NW; ++g) part[g][r] = ld_cluster4(at + g * kRows * 4);
+          }
+        int sum[NW][4] = {};
+#pragma unroll
+        for (int r = 0; r < kMaxSplit; ++r)
+          if (r < split)
+#pragma unroll
+            for (int g = 0; g < NW; ++g) {
+              sum[g][0] += part[g][r].x;
+              sum[g][1] += part[g][r].y;
+              sum[g][2] += part[g][r].z;
+              sum[g][3] += part[g][r].w;
             }
+        const float sx = s_sx[t];
+        uint32_t o[4];
 #pragma unroll
-          for (int r = 0; r < kMaxSplit; ++r)
-            if (r < split)
+        for (int e = 0; e < 4; ++e) {
+          float v = w8a8_scaled(sum[0][e], sx, sw[0][e]);
+          if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1][e], sx, sw[NW - 1][e]));
+          else v += bias[e];
+          o[e] = to_16<F16>(v);
+        }
+        uint16_t* dst = A.y + (size_t)(m0 + t) * A.d_out + n;
+        if ((A.d_out & 3) == 0) {
+          if (n < A.d_out) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+        } else {
 #pragma unroll
-              for (int g = 0; g < NW; ++g) sum[g] += part[g][r];
-          store(t, sum);
+          for (int e = 0; e < 4; ++e)
+            if (n + e < A.d_out) dst[e] = (uint16_t)o[e];
         }
       }
     }
-    __syncwarp();
+  }
+  __syncwarp();
+  if (split > 1) {
     cluster_arrive();  // the others' sums are read: their CTAs may end
     cluster_wait();
   }
@@ -267,24 +280,27 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages > per) stages = per;
   int bytes = stages * Geo::STAGE;
-  if (split > 1 && bytes < Geo::SUMS) bytes = Geo::SUMS;
+  if (bytes < Geo::SUMS) bytes = Geo::SUMS;
   A.stages = stages;
   bytes += 1024;
   auto kernel = w8a8_few_kernel<TN, GATED, F16>;
-  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), bytes);
+  static std::atomic<uint64_t> limit{0};
+  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kMaxSmem, limit);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * split, mtiles);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = split;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, A, status);
 }
 

@@ -9,8 +9,10 @@
 //   warp 0    TMA: its halves of a stage, completing on the first CTA's barrier;
 //   warp 1    MMA (first CTA only): four tcgen05.mma 256 x 256 x 32 a stage on
 //             both SMs, then a commit that frees the stage in both CTAs;
-//   warps 2-5 epilogue: thread = token, 32 columns at a time; scales, gate or
-//             bias, rounding, 16-byte stores.
+//   warps 2-9 epilogue: thread = token, half of the tile's channels, 32 at a
+//             time; scales, gate or bias, rounding, then through shared memory
+//             (64-byte swizzle) and a TMA store, which writes whole sectors and
+//             leaves out what lies outside y.
 // Two sets of sums (2 x 256 columns of tensor memory) let the next tile's MMAs
 // run under a tile's epilogue.  Every wait is bounded.
 #include "int8.cuh"
@@ -23,12 +25,14 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 256, kHalf = 128, kK = 128, kThreads = 192, kStages = 6;
+constexpr int kTile = 256, kHalf = 128, kK = 128, kStages = 6;
+constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
+constexpr int kOutBytes = 32 * 64;  // a warp's 32 tokens x 32 channels on their way out
 constexpr int kHalfBytes = kHalf * kK, kStageBytes = 2 * kHalfBytes;
-constexpr int kSmem = kStages * kStageBytes + 1024;
+constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kOutBytes + 1024;
 
 struct ManyArgs {
-  CUtensorMap q, w, w2;
+  CUtensorMap q, w, w2, out;  // out: y in boxes of 32 x 32, where its rows are a multiple of 16 bytes
   const float* sx;
   const float* sw;
   const float* sw2;
@@ -66,7 +70,7 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(b_acc_full + 8 * s, 1);
-      mbar_init(b_acc_empty + 8 * s, 8);  // (first CTA) the epilogue warps of both CTAs
+      mbar_init(b_acc_empty + 8 * s, 2 * kEpiWarps);  // (first CTA) the epilogue warps of both CTAs
     }
     abort_flag = 0;
     s_issued = 0;
@@ -80,6 +84,8 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
   cluster_wait();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  grid_trigger();
+  grid_wait();  // the kernel before is done: what follows reads and writes
 
   auto fail = [&]() {
     report_status(status, kStatusTimeout);
@@ -137,7 +143,9 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       s_committed = it;
     }
   } else {
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    unsigned char* out = smem + kStages * kStageBytes + (warp - 2) * kOutBytes;
+    const bool by_tma = (A.d_out & 7) == 0;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     int j = 0;
 #pragma unroll 1
@@ -147,24 +155,22 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       const float sx = m < A.M ? A.sx[m] : 0.0f;
       // the tile's channel values, while its MMAs run; two sets, so that a warp
       // may be one tile ahead of another
-      for (int c = threadIdx.x - 64; c < kTile; c += 128) {
+      for (int c = threadIdx.x - 64; c < kTile; c += 32 * kEpiWarps) {
         const bool up = GATED && c >= kHalf;
         const int n = n0 + (up ? c - kHalf : c);
         s_sw[acc][c] = n < A.d_out ? (up ? A.sw2 : A.sw)[n] : 0.0f;
         if constexpr (!GATED) s_bias[acc][c] = A.bias && n < A.d_out ? from_16<F16>(A.bias[n]) : 0.0f;
       }
-      asm volatile("bar.sync 1, 128;\n" ::: "memory");
+      asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kEpiWarps) : "memory");
       if (!mbar_wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
       tc_fence_after();
 #pragma unroll 1
-      for (int c0 = 0; c0 < NC && n0 + c0 < A.d_out; c0 += 32) {
+      for (int c0 = half * (NC / 2); c0 < (half + 1) * (NC / 2) && n0 + c0 < A.d_out; c0 += 32) {
         int v[32], u[GATED ? 32 : 1];
         tmem_ld(lanes + acc * kTile + c0, v);
         if constexpr (GATED) tmem_ld(lanes + acc * kTile + kHalf + c0, u);
         tmem_ld_wait();
-        if (m >= A.M) continue;
         const int n = n0 + c0;
-        uint16_t* dst = A.y + (size_t)m * A.d_out + n;
         uint32_t o[16];
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
@@ -184,20 +190,34 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
           o[c / 2] = to_16<F16>(f[0]) | ((uint32_t)to_16<F16>(f[1]) << 16);
           o[c / 2 + 1] = to_16<F16>(f[2]) | ((uint32_t)to_16<F16>(f[3]) << 16);
         }
-        if (n + 32 <= A.d_out && (A.d_out & 7) == 0) {
+        // row = token, 64 bytes, its 16-byte parts swapped by bits 1-2 of the row
+        bulk_read_wait();  // the last box has left this warp's part
+        __syncwarp();
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4*>(dst)[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(out + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+              make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        const int m_warp = m - lane;
+        if (by_tma) {
+          async_fence();
+          __syncwarp();
+          if (lane == 0 && m_warp < A.M) {
+            tma_store(&A.out, smem_u32(out), n, m_warp);
+            bulk_commit();
+          }
         } else {
-#pragma unroll
-          for (int c = 0; c < 32; ++c)
-            if (n + c < A.d_out) dst[c] = (uint16_t)(o[c >> 1] >> (16 * (c & 1)));
+          __syncwarp();
+          for (int r = 0; r < 32 && m_warp + r < A.M; ++r)
+            if (n + lane < A.d_out)
+              A.y[(size_t)(m_warp + r) * A.d_out + n + lane] = *reinterpret_cast<const uint16_t*>(
+                  out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
         }
       }
       __syncwarp();
       tc_fence_before();
       if (lane == 0) mbar_arrive_cluster(mapa(b_acc_empty + 8 * acc, 0));
     }
+    bulk_wait();
   }
 
   // ---- teardown ----------------------------------------------------------------------
@@ -241,11 +261,21 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
 template <bool GATED, bool F16>
 cudaError_t launch_many(const ManyArgs& A, int* status, cudaStream_t s) {
   auto kernel = w8a8_many_kernel<GATED, F16>;
-  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kSmem);
+  static std::atomic<uint64_t> limit{0};
+  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kSmem, limit);
   if (e != cudaSuccess) return e;
   const int pairs = device_sm_count() / 2;
-  kernel<<<2 * (A.tiles < pairs ? A.tiles : pairs), kThreads, kSmem, s>>>(A, status);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * (A.tiles < pairs ? A.tiles : pairs));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, A, status);
 }
 
 }  // namespace
@@ -255,6 +285,7 @@ cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream
   if (!w8_map(&A.q, a.q, a.M, a.d_in, kHalf) || !w8_map(&A.w, a.w, a.d_out, a.d_in, kHalf) ||
       (a.w2 && !w8_map(&A.w2, a.w2, a.d_out, a.d_in, kHalf)))
     return cudaErrorInvalidValue;
+  if (a.d_out % 8 == 0 && !w8_out_map(&A.out, a.y, a.M, a.d_out)) return cudaErrorInvalidValue;
   A.sx = a.sx;
   A.sw = a.sw;
   A.sw2 = a.sw2;
