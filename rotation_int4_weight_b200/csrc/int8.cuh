@@ -2,9 +2,15 @@
 // row, and the int8 x int8 linears on them.
 #pragma once
 
+#include <atomic>
+
 #include "paro_internal.cuh"
 
 namespace paro {
+
+// Allows a kernel up to `bytes` of dynamic shared memory on the current device,
+// once for each device (`done` has a bit for each, and is the kernel's own).
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 // ---- int8_codes.cu ---------------------------------------------------------------
 // Row codes of 16-bit activations [M][d], any d >= 1: with `norm` the RMS norm

@@ -11,21 +11,24 @@
 //   look at the row's statistics.
 //
 // Codes are exact.  h g of two bf16 (16 bits) or fp16 (22 bits) values is exact
-// in fp32 (unless it underflows), and so is an fp32 weight.  t = v * (127 / a)
-// in fp32 is within 127 * 2^-22 = 3.1e-5 of 127 v / a; only where t lies within
-// 2^-13 of a border k + 1/2 (about one value in 4000) does the comparison
-// 254 |v| against (2k + 1) a decide, in fp64, where both products are exact (32
-// bits at most).  So the codes do not depend on the order of any sum.
+// in fp32 (unless it underflows), and so is an fp32 weight.  v * (127 / a) with
+// the quotient rounded to fp32 is within 127 * 2^-24 = 7.6e-6 of 127 v / a; only
+// where it lies within 2^-16 of a border k + 1/2 (about one value in 30000) does
+// the comparison of 254 |v| with (2k + 1) a decide, in fp64, where both products
+// are exact (32 bits at most).  So the codes do not depend on any sum's order.
 //
-// A row is read once, kept in registers as 8-value chunks, and its codes are
-// written from there: 3 bytes a value, 7 with a residual.  Bound by HBM for
-// many rows, by one row's latency (load, reduction, store) for few.  Chunks are
-// cut at multiples of 8 of the flat index, not of the column, so that rows of
-// an odd width still move as 16-byte loads and 8-byte stores; the first and
-// last chunk of such a row go value by value, and its gain comes from two
-// aligned 16-byte loads shifted by the row's phase.
+// A row is read once, kept in registers as 16-value chunks, and its codes are
+// written from there: 3 bytes a value, 7 with a residual.  Chunks are cut at
+// multiples of 16 of the flat index, not of the column, so that rows of an odd
+// width still move as 16-byte loads and stores; the first and last chunk of such
+// a row go value by value, and its gain comes from aligned 16-byte loads shifted
+// by the row's phase.  For many rows the instructions, about 10 a value, and HBM
+// bound it alike: 2048 x 4096 bf16 with a residual in 13.7 us (4.3 TB/s), 4096 x
+// 8192 in 43.7 us (5.4 TB/s), packing 14336 x 4096 fp32 in 44.4 us (6.6 TB/s);
+// for one row its latency does (2.5 us).
 #include "int8.cuh"
 #include "tc_ptx.cuh"
+#include "w4_stream.cuh"  // device_sm_count
 
 namespace paro {
 namespace {
@@ -42,113 +45,201 @@ struct CodeArgs {
   float eps;
 };
 
-__device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
-__device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
-__device__ __forceinline__ float to_f32(float v) { return v; }
-__device__ __forceinline__ void from_f32(float f, __nv_bfloat16& o) { o = __float2bfloat16_rn(f); }
-__device__ __forceinline__ void from_f32(float f, __half& o) { o = __float2half_rn(f); }
-__device__ __forceinline__ void from_f32(float f, float& o) { o = f; }
+constexpr int kW = 16;  // values of a chunk
 
-// Eight consecutive values of one row.
+// kW consecutive values of one row, as they lie in memory.
 template <typename T>
 struct __align__(16) Chunk {
-  T v[8];
+  uint32_t w[kW * sizeof(T) / 4];
 };
+
+__device__ __forceinline__ float value(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ float value(__half v) { return __half2float(v); }
+__device__ __forceinline__ float value(float v) { return v; }
+
+__device__ __forceinline__ void values(const Chunk<__nv_bfloat16>& c, float (&v)[kW]) {
+#pragma unroll
+  for (int i = 0; i < kW / 2; ++i) {
+    v[2 * i] = __uint_as_float(c.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(c.w[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void values(const Chunk<__half>& c, float (&v)[kW]) {
+#pragma unroll
+  for (int i = 0; i < kW / 2; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&c.w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void values(const Chunk<float>& c, float (&v)[kW]) {
+#pragma unroll
+  for (int i = 0; i < kW; ++i) v[i] = __uint_as_float(c.w[i]);
+}
+
+// a + b, rounded to T.
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __nv_bfloat16) {
+  const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi, __half) {
+  const __half2 b = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&b);
+}
+template <typename T>
+__device__ __forceinline__ void add_to(Chunk<T>& a, const Chunk<T>& b) {
+  float x[kW], y[kW];
+  values(a, x);
+  values(b, y);
+#pragma unroll
+  for (int i = 0; i < kW / 2; ++i)
+    a.w[i] = pack2(__fadd_rn(x[2 * i], y[2 * i]), __fadd_rn(x[2 * i + 1], y[2 * i + 1]), T());
+}
+template <typename T>
+__device__ __forceinline__ void times(float (&v)[kW], const Chunk<T>& g) {
+  float f[kW];
+  values(g, f);
+#pragma unroll
+  for (int e = 0; e < kW; ++e) v[e] = __fmul_rn(v[e], f[e]);
+}
 
 template <typename T>
 __device__ __forceinline__ Chunk<T> load_vec(const T* p) {
   Chunk<T> c;
-  const uint4* s = reinterpret_cast<const uint4*>(p);
-  uint4* o = reinterpret_cast<uint4*>(&c);
 #pragma unroll
-  for (int i = 0; i < (int)(sizeof(Chunk<T>) / 16); ++i) o[i] = s[i];
-  return c;
-}
-
-// Values lo .. hi - 1 of the chunk at p (the others zero), one by one.
-template <typename T>
-__device__ __forceinline__ Chunk<T> load_part(const T* p, int lo, int hi) {
-  Chunk<T> c;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    from_f32(0.0f, c.v[e]);
-    if (e >= lo && e < hi) c.v[e] = p[e];
+  for (int i = 0; i < (int)(sizeof(c) / 16); ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    c.w[4 * i] = u.x, c.w[4 * i + 1] = u.y, c.w[4 * i + 2] = u.z, c.w[4 * i + 3] = u.w;
   }
   return c;
 }
+template <typename T>
+__device__ __forceinline__ void store_vec(T* p, const Chunk<T>& c) {
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(c) / 16); ++i)
+    reinterpret_cast<uint4*>(p)[i] = make_uint4(c.w[4 * i], c.w[4 * i + 1], c.w[4 * i + 2], c.w[4 * i + 3]);
+}
 
-// gain[c .. c + 7], columns outside 0 .. d - 1 zero.  c & 7 is the same for
+// Values lo .. hi - 1 of the chunk at p (the others zero), one by one.
+__device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) { return *reinterpret_cast<const uint16_t*>(p); }
+__device__ __forceinline__ uint32_t bits(const __half* p) { return *reinterpret_cast<const uint16_t*>(p); }
+__device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_part(const T* p, int lo, int hi) {
+  Chunk<T> c = {};
+#pragma unroll
+  for (int e = 0; e < kW; ++e)
+    if (e >= lo && e < hi) c.w[e * sizeof(T) / 4] |= bits(p + e) << (sizeof(T) == 2 ? 16 * (e & 1) : 0);
+  return c;
+}
+template <typename T>
+__device__ __forceinline__ void store_part(T* p, const Chunk<T>& c, int lo, int hi) {
+#pragma unroll
+  for (int e = 0; e < kW; ++e)
+    if (e >= lo && e < hi) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(c.w[e / 2] >> (16 * (e & 1)));
+}
+
+// gain[c .. c + kW - 1], columns outside 0 .. d - 1 zero.  c & 7 is the same for
 // all chunks of a row.
 template <typename T>
 __device__ __forceinline__ Chunk<T> load_gain(const T* g, int c, int d) {
   const int a = c & ~7, sh = c & 7;
-  if (a < 0 || a + (sh ? 16 : 8) > d) return load_part(g + c, -c, d - c);
-  const Chunk<T> A = load_vec(g + a);
-  if (sh == 0) return A;
-  const Chunk<T> B = load_vec(g + a + 8);
-  uint32_t w[8];
-  const uint32_t* pa = reinterpret_cast<const uint32_t*>(&A);
-  const uint32_t* pb = reinterpret_cast<const uint32_t*>(&B);
+  if (a < 0 || a + kW + 8 > d) return load_part(g + c, -c, d - c);
+  uint32_t w[kW / 2 + 4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = pa[i];
-    w[4 + i] = pb[i];
+  for (int i = 0; i < (kW + 8) / 8; ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(g + a)[i];
+    w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
   }
   if (sh & 4) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    for (int i = 0; i < kW / 2 + 2; ++i) w[i] = w[i + 2];
   }
   if (sh & 2) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    for (int i = 0; i < kW / 2 + 1; ++i) w[i] = w[i + 1];
   }
   if (sh & 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    for (int i = 0; i < kW / 2; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
   }
   Chunk<T> o;
-  uint32_t* po = reinterpret_cast<uint32_t*>(&o);
 #pragma unroll
-  for (int i = 0; i < 4; ++i) po[i] = w[i];
+  for (int i = 0; i < kW / 2; ++i) o.w[i] = w[i];
   return o;
 }
 
-// The code of v where t = v * (127 / a) lies next to a border between two codes.
-__device__ __noinline__ int border_code(float v, float a, float t) {
-  const int k = (int)fabsf(t);  // t is near k + 1/2: the whole part is certain
+// The largest magnitude met so far, as bits: of two 16-bit values side by side, or
+// of one fp32.  Magnitudes order as unsigned numbers, infinity and NaN last.
+template <typename T>
+__device__ __forceinline__ uint32_t widest(uint32_t m, const Chunk<T>& c) {
+  constexpr uint32_t kMask = sizeof(T) == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu;
+#pragma unroll
+  for (int i = 0; i < (int)(kW * sizeof(T) / 4); i += 2) {
+    if constexpr (sizeof(T) == 2) m = __vimax3_u16x2(m, c.w[i] & kMask, c.w[i + 1] & kMask);
+    else m = __vimax3_u32(m, c.w[i] & kMask, c.w[i + 1] & kMask);
+  }
+  return m;
+}
+// The wider of the two halves as fp32 bits.
+__device__ __forceinline__ uint32_t widest_bits(uint32_t m, __nv_bfloat16) { return max(m & 0xFFFFu, m >> 16) << 16; }
+__device__ __forceinline__ uint32_t widest_bits(uint32_t m, __half) {
+  return __float_as_uint(__half2float(__ushort_as_half((unsigned short)max(m & 0xFFFFu, m >> 16))));
+}
+__device__ __forceinline__ uint32_t widest_bits(uint32_t m, float) { return m; }
+
+// The code of v where 127 v / a lies next to a border between two codes.
+__device__ __noinline__ float border_code(float v, float a, float inv) {
+  const int k = (int)fabsf(__fmul_rn(v, inv));  // near k + 1/2: the whole part is certain
   const double lhs = 254.0 * (double)fabsf(v), rhs = (double)(2 * k + 1) * (double)a;
   const int m = lhs > rhs ? k + 1 : (lhs < rhs ? k : k + (k & 1));
-  return v < 0.0f ? -m : m;
+  return v < 0.0f ? -(float)m : (float)m;
 }
 
-// Codes of eight values; `up` scales v and a alike (a power of two) so that
-// 127 / a stays finite for rows of the smallest magnitudes.
-__device__ __forceinline__ uint2 code8(const float (&v)[8], float a, float inv, float up) {
-  int q[8];
-  bool near = false;
-  float t[8];
+// Codes of a chunk's values.  Adding 1.5 * 2^23 rounds to a whole number, ties to
+// even, and leaves it in the sum's low bits.
+__device__ __forceinline__ uint4 codes_of(const float (&v)[kW], float a, float inv) {
+  constexpr float kWhole = 12582912.0f, kNear = 0.5f - 0x1p-16f;
+  uint32_t o[kW / 4];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    t[e] = __fmul_rn(__fmul_rn(v[e], up), inv);
-    const float k = rintf(t[e]);
-    near |= fabsf(__fsub_rn(t[e], k)) > 0.5f - 0x1p-13f;
-    q[e] = (int)k;
-  }
-  if (near) {
+  for (int i = 0; i < kW; i += 4) {
+    float m[4], off[4];
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      if (fabsf(__fsub_rn(t[e], rintf(t[e]))) > 0.5f - 0x1p-13f) q[e] = border_code(__fmul_rn(v[e], up), a, t[e]);
+    for (int e = 0; e < 4; ++e) {
+      m[e] = __fmaf_rn(v[i + e], inv, kWhole);
+      off[e] = __fmaf_rn(v[i + e], inv, -__fsub_rn(m[e], kWhole));
+    }
+    // three-input minima and maxima
+    const float lo = fminf(fminf(fminf(off[0], off[1]), off[2]), off[3]);
+    const float hi = fmaxf(fmaxf(fmaxf(off[0], off[1]), off[2]), off[3]);
+    if (fmaxf(hi, -lo) > kNear) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (fabsf(off[e]) > kNear) m[e] = __fadd_rn(border_code(v[i + e], a, inv), kWhole);
+    }
+    o[i / 4] = __byte_perm(__byte_perm(__float_as_uint(m[0]), __float_as_uint(m[1]), 0x0040),
+                           __byte_perm(__float_as_uint(m[2]), __float_as_uint(m[3]), 0x0040), 0x5410);
   }
-  uint2 o;
-  o.x = (q[0] & 0xFF) | ((q[1] & 0xFF) << 8) | ((q[2] & 0xFF) << 16) | ((uint32_t)q[3] << 24);
-  o.y = (q[4] & 0xFF) | ((q[5] & 0xFF) << 8) | ((q[6] & 0xFF) << 16) | ((uint32_t)q[7] << 24);
-  return o;
+  return make_uint4(o[0], o[1], o[2], o[3]);
 }
+
+// A row's scale, in fp64: a product that leaves fp32's range on the way cannot
+// spoil it.  ss: the sum of (hs h)^2.
+template <bool NORM>
+__device__ __forceinline__ float row_scale(float amax, bool finite, float ss, float hs, int d, float eps) {
+  if (!finite) return __int_as_float(0x7FC00000);
+  if (amax == 0.0f) return 1.0f;
+  const double s = (double)amax / 127.0;
+  return (float)(NORM ? s / sqrt((double)ss / ((double)hs * hs) / d + (double)eps) : s);
+}
+
+// True where fp32 sums of squares overflowed, or lost digits to underflow.
+__device__ __forceinline__ bool out_of_range(float ss) { return !(ss <= 3.0e38f) || ss < 0x1p-90f; }
 
 // threadIdx.x runs over a row's chunks (NC of them a thread, blockDim.x apart),
 // threadIdx.y over the rows of the CTA (more than one only at 32 threads a row).
-// EVEN: d is a multiple of 8, every chunk is whole and starts at a column
-// multiple of 8.
+// EVEN: d is a multiple of kW, every chunk is whole and starts at a column
+// multiple of kW.
 template <typename T, int NC, bool NORM, bool EVEN>
 __global__ void __launch_bounds__(1024)
 codes_kernel(const CodeArgs A) {
@@ -159,145 +250,143 @@ codes_kernel(const CodeArgs A) {
   const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= A.M) return;  // whole warps: a CTA of several rows has one warp for each and no barrier
   const int d = A.d, T1 = blockDim.x;
-  const long long base = row * d, first = base & ~7LL;  // flat index of the row, of its first chunk
-  const int head = (int)(base - first);
-  const int chunks = (head + d + 7) >> 3;
+  const long long base = row * d, first = EVEN ? base : base & ~(long long)(kW - 1);  // flat index of the row, of its first chunk
+  const int head = EVEN ? 0 : (int)(base - first);
+  const int chunks = (head + d + kW - 1) / kW;
+  const bool with_res = NORM && A.residual != nullptr, with_gain = NORM && A.gain != nullptr;
   const T* x = static_cast<const T*>(A.x) + first;
-  const T* res = static_cast<const T*>(A.residual) + (A.residual ? first : 0);
+  const T* res = static_cast<const T*>(A.residual) + (with_res ? first : 0);
   const T* gain = static_cast<const T*>(A.gain);
-  T* hid = static_cast<T*>(A.hidden) + (A.hidden ? first : 0);
+  T* hid = static_cast<T*>(A.hidden) + (with_res ? first : 0);
   int8_t* q = A.q + first;
 
+  // All loads of a thread come before its first store (hidden may be x or the
+  // residual, so the compiler would keep their order), to be in flight together.
+  // Values stay packed and are multiplied by their gains twice: registers decide
+  // how many rows an SM has in flight.
   Chunk<T> h[NC];
-  // the loads of all chunks first, so that they are in flight together
+  {
+    [[maybe_unused]] Chunk<T> r[NORM ? NC : 1];
 #pragma unroll
-  for (int i = 0; i < NC; ++i) {
-    const int j = threadIdx.x + i * T1, c = j * 8 - head;
-    if (j < chunks) {
-      if (EVEN || (c >= 0 && c + 8 <= d)) h[i] = load_vec(x + j * 8);
-      else h[i] = load_part(x + j * 8, -c, d - c);
+    for (int i = 0; i < NC; ++i) {
+      const int j = threadIdx.x + i * T1, c = j * kW - head;
+      if (j < chunks) {
+        const bool whole = EVEN || (c >= 0 && c + kW <= d);
+        h[i] = whole ? load_vec(x + j * kW) : load_part(x + j * kW, -c, d - c);
+        if constexpr (NORM)
+          if (with_res) r[i] = whole ? load_vec(res + j * kW) : load_part(res + j * kW, -c, d - c);
+      }
     }
+    if constexpr (NORM)
+      if (with_res) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int j = threadIdx.x + i * T1, c = j * kW - head;
+          if (j < chunks) {
+            add_to(h[i], r[i]);
+            if (EVEN || (c >= 0 && c + kW <= d)) store_vec(hid + j * kW, h[i]);
+            else store_part(hid + j * kW, h[i], -c, d - c);
+          }
+        }
+      }
   }
-  uint32_t amax = 0u;  // bits of the largest |v|: inf and NaN order above every number
+  // the values of a chunk whose codes are wanted
+  auto row_values = [&](int i, int j, float (&v)[kW]) {
+    values(h[i], v);
+    if constexpr (NORM)
+      if (with_gain) times(v, EVEN ? load_vec(gain + j * kW) : load_gain(gain, j * kW - head, d));
+  };
+  uint32_t wide = 0u;  // bits of the largest |v|
   float ss = 0.0f;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int j = threadIdx.x + i * T1, c = j * 8 - head;
+    const int j = threadIdx.x + i * T1;
     if (j < chunks) {
-      const bool whole = EVEN || (c >= 0 && c + 8 <= d);
-      if (NORM && A.residual) {
-        const Chunk<T> r = whole ? load_vec(res + j * 8) : load_part(res + j * 8, -c, d - c);
+      if constexpr (NORM) {
+        float v[kW];
+        values(h[i], v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) from_f32(__fadd_rn(to_f32(h[i].v[e]), to_f32(r.v[e])), h[i].v[e]);
-        if (whole) {
+        for (int e = 0; e < kW; ++e) ss = fmaf(v[e], v[e], ss);
+        if (with_gain) times(v, EVEN ? load_vec(gain + j * kW) : load_gain(gain, j * kW - head, d));
+        Chunk<float> c;
 #pragma unroll
-          for (int w = 0; w < (int)(sizeof(Chunk<T>) / 16); ++w)
-            reinterpret_cast<uint4*>(hid + j * 8)[w] = reinterpret_cast<const uint4*>(&h[i])[w];
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e)
-            if (c + e >= 0 && c + e < d) hid[j * 8 + e] = h[i].v[e];
-        }
-      }
-      if (NORM && A.gain) {
-        const Chunk<T> g = EVEN ? load_vec(gain + j * 8) : load_gain(gain, c, d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = to_f32(h[i].v[e]);
-          ss = fmaf(f, f, ss);
-          amax = max(amax, __float_as_uint(fabsf(__fmul_rn(f, to_f32(g.v[e])))));
-        }
+        for (int e = 0; e < kW; ++e) c.w[e] = __float_as_uint(v[e]);
+        wide = widest(wide, c);
       } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = to_f32(h[i].v[e]);
-          if (NORM) ss = fmaf(f, f, ss);
-          amax = max(amax, __float_as_uint(fabsf(f)));
-        }
+        wide = widest(wide, h[i]);
       }
     }
   }
+  if constexpr (!NORM) wide = widest_bits(wide, T());
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = T1 >> 5;
-  auto row_sum = [&](float v) {
+  // both reductions at once
+  auto reduce = [&]() {
+    wide = __reduce_max_sync(0xffffffffu, wide);
+    if (NORM) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    if (warps > 1) {
-      if (lane == 0) red_s[warp] = v;
-      __syncthreads();
-      v = lane < warps ? red_s[lane] : 0.0f;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+      for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     }
-    return v;
-  };
-  amax = __reduce_max_sync(0xffffffffu, amax);
-  if (warps > 1 && lane == 0) red_a[warp] = amax;
-  if (NORM) ss = row_sum(ss);
-  else if (warps > 1) __syncthreads();
-  if (warps > 1) amax = __reduce_max_sync(0xffffffffu, lane < warps ? red_a[lane] : 0u);
-
-  const bool finite = amax < 0x7F800000u;
-  // sums of squares beyond fp32's range, or so small that they lost digits,
-  // once more on h scaled by a power of two (uniform over the row)
-  float hs = 1.0f;
-  if (NORM && finite && amax != 0u && (!(ss <= 3.0e38f) || ss < 0x1p-90f)) {
-    hs = ss < 1.0f ? 0x1p+80f : 0x1p-80f;
-    float s2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NC; ++i)
-      if ((int)threadIdx.x + i * T1 < chunks) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float f = to_f32(h[i].v[e]) * hs;
-          s2 = fmaf(f, f, s2);
-        }
+    if (warps > 1) {
+      if (lane == 0) {
+        red_a[warp] = wide;
+        if (NORM) red_s[warp] = ss;
       }
-    if (warps > 1) __syncthreads();  // red_s is read above
-    ss = row_sum(s2);
+      __syncthreads();
+      wide = __reduce_max_sync(0xffffffffu, lane < warps ? red_a[lane] : 0u);
+      if (NORM) {
+        ss = lane < warps ? red_s[lane] : 0.0f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      }
+    }
+  };
+  reduce();
+  const float amax = __uint_as_float(wide);
+  const bool finite = wide < 0x7F800000u;
+  // sums of squares beyond fp32's range, or so small that they lost digits,
+  // once more on h scaled by a power of two (uniform over the row, and rare)
+  float hs = 1.0f;
+  if (NORM && finite && amax != 0.0f && out_of_range(ss)) {
+    hs = ss < 1.0f ? 0x1p+80f : 0x1p-80f;
+    ss = 0.0f;
+    const T* hp = with_res ? hid : x;
+    for (int j = threadIdx.x; j < chunks; j += T1)
+      for (int e = 0; e < kW; ++e) {
+        const int c = j * kW - head + e;
+        const float f = c >= 0 && c < d ? value(hp[j * kW + e]) * hs : 0.0f;
+        ss = fmaf(f, f, ss);
+      }
+    if (warps > 1) __syncthreads();  // the first sums have been read
+    reduce();
   }
 
-  const float up = __uint_as_float(amax) < 0x1p-100f ? 0x1p+100f : 1.0f;
-  const float a = __uint_as_float(amax) * up;
-  const float inv = finite && amax != 0u ? __fdiv_rn(127.0f, a) : 0.0f;
+  // rows that are not finite get codes 0; for the smallest magnitudes v and a are
+  // taken a power of two larger, so that 127 / a stays in fp32's range
+  const float up = amax < 0x1p-100f ? 0x1p+100f : 1.0f;
+  const float a = amax * up, inv = finite && amax != 0.0f ? __fdiv_rn(127.0f, a) : 0.0f;
 #pragma unroll
   for (int i = 0; i < NC; ++i) {
-    const int j = threadIdx.x + i * T1, c = j * 8 - head;
+    const int j = threadIdx.x + i * T1, c = j * kW - head;
     if (j < chunks) {
-      float v[8];
+      float v[kW];
+      row_values(i, j, v);
+      if (!finite || up != 1.0f) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = to_f32(h[i].v[e]);
-      if (NORM && A.gain) {
-        const Chunk<T> g = EVEN ? load_vec(gain + j * 8) : load_gain(gain, c, d);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = __fmul_rn(v[e], to_f32(g.v[e]));
+        for (int e = 0; e < kW; ++e) v[e] = finite ? v[e] * up : 0.0f;
       }
-      if (!finite) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      }
-      const uint2 o = code8(v, a, inv, up);
-      if (EVEN || (c >= 0 && c + 8 <= d)) {
-        *reinterpret_cast<uint2*>(q + j * 8) = o;
+      const uint4 o = codes_of(v, a, inv);
+      if (EVEN || (c >= 0 && c + kW <= d)) {
+        *reinterpret_cast<uint4*>(q + j * kW) = o;
       } else {
+        const uint32_t w[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (c + e >= 0 && c + e < d) q[j * 8 + e] = (int8_t)((e < 4 ? o.x : o.y) >> (8 * (e & 3)));
+        for (int e = 0; e < kW; ++e)
+          if (c + e >= 0 && c + e < d) q[j * kW + e] = (int8_t)(w[e / 4] >> (8 * (e & 3)));
       }
     }
   }
-  if (threadIdx.x == 0) {
-    // one thread, after the codes: r in fp64 (a product that leaves fp32's range
-    // on the way cannot spoil the scale)
-    double s = 1.0;
-    if (!finite) {
-      s = __longlong_as_double(0x7FF8000000000000LL);
-    } else if (amax != 0u) {
-      s = (double)__uint_as_float(amax) / 127.0;
-      if (NORM) s /= sqrt((double)ss / ((double)hs * hs) / d + (double)A.eps);
-    }
-    A.sx[row] = (float)s;
-  }
+  if (threadIdx.x == 0) A.sx[row] = row_scale<NORM>(amax, finite, ss, hs, d, A.eps);
 }
 
 template <typename T, bool NORM, bool EVEN>
@@ -314,20 +403,26 @@ cudaError_t launch_nc(const CodeArgs& A, int nc, int threads, cudaStream_t s) {
   cfg.numAttrs = 1;
   if (nc <= 1) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 1, NORM, EVEN>, A);
   if (nc <= 2) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 2, NORM, EVEN>, A);
-  if (nc <= 4) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 4, NORM, EVEN>, A);
-  return cudaLaunchKernelEx(&cfg, codes_kernel<T, 8, NORM, EVEN>, A);
+  return cudaLaunchKernelEx(&cfg, codes_kernel<T, 4, NORM, EVEN>, A);
 }
 
 template <typename T, bool NORM>
 cudaError_t launch_rows(const CodeArgs& A, cudaStream_t s) {
-  const int chunks = A.d % 8 ? A.d / 8 + 2 : A.d / 8;
-  const int nc = A.M <= 296 ? 1 : 4;
-  int threads = (chunks + nc - 1) / nc;
-  threads = (threads + 31) / 32 * 32;
+  // Chunks a thread takes.  One while all rows' threads fit the GPU at once, where
+  // a row's latency counts.  Else each row costs its threads the same instructions
+  // for addresses, reduction and scale, so fewer threads with more chunks gain,
+  // until too few rows are in flight or registers run out.  Measured, us, with
+  // 1, 2, 4 chunks (bf16): norm 2048 x 4096: 15.6, 13.7, 18.1; 4096 x 8192: 54.7,
+  // 43.7, 54.0; codes 2048 x 1536: 4.7, 6.9, 8.5; 4096 x 8192: 25.2, 23.9, 23.2;
+  // 2048 x 14336: 32.8, 23.9, 21.5; fp32 14336 x 4096: 45.0, 44.4, 62.1.
+  const int chunks = A.d % kW ? A.d / kW + 2 : A.d / kW;
+  const bool few = A.M * chunks <= (long long)device_sm_count() * 1024;
+  const int want = few ? 1 : NORM || sizeof(T) == 4 ? 2 : chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4;
+  int threads = ((chunks + want - 1) / want + 31) / 32 * 32;
   if (threads > 1024) threads = 1024;
   const int need = (chunks + threads - 1) / threads;
-  if (need > 8) return cudaErrorInvalidValue;
-  return A.d % 8 == 0 ? launch_nc<T, NORM, true>(A, need, threads, s) : launch_nc<T, NORM, false>(A, need, threads, s);
+  if (need > 4) return cudaErrorInvalidValue;
+  return A.d % kW == 0 ? launch_nc<T, NORM, true>(A, need, threads, s) : launch_nc<T, NORM, false>(A, need, threads, s);
 }
 
 }  // namespace
@@ -341,15 +436,8 @@ cudaError_t launch_int8_codes(const uint16_t* x, const uint16_t* residual, const
 }
 
 cudaError_t launch_int8_pack(const float* W, int8_t* q, float* s, int rows, int d, cudaStream_t stream) {
-  if (d % 8) return cudaErrorInvalidValue;
   const CodeArgs A{W, nullptr, nullptr, nullptr, q, s, rows, d, 0.0f};
-  const int chunks = d / 8, nc = rows <= 296 ? 1 : 4;
-  int threads = (chunks + nc - 1) / nc;
-  threads = (threads + 31) / 32 * 32;
-  if (threads > 1024) threads = 1024;
-  const int need = (chunks + threads - 1) / threads;
-  if (need > 8) return cudaErrorInvalidValue;
-  return launch_nc<float, false, true>(A, need, threads, stream);
+  return launch_rows<float, false>(A, stream);
 }
 
 }  // namespace paro

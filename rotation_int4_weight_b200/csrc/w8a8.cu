@@ -5,7 +5,6 @@
 // exact 32-bit integers (|sum| <= 49152 * 2^14 < 2^31), so they do not depend on
 // any order; what follows is fp32 and one rounding to y's type.
 #include <atomic>
-#include <cstdlib>
 
 #include "int8.cuh"
 #include "w8a8.cuh"
@@ -52,7 +51,7 @@ bool w8_out_map(CUtensorMap* map, const uint16_t* y, int rows, int d_out) {
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-cudaError_t w8_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -64,7 +63,7 @@ cudaError_t w8_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& 
 }
 
 cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream) {
-  if (getenv("W8F") ? a.M <= atoi(getenv("W8F")) : a.M <= 128) return launch_w8a8_few(a, status, stream);
+  if (a.M <= 128) return launch_w8a8_few(a, status, stream);
   return launch_w8a8_many(a, status, stream);
 }
 

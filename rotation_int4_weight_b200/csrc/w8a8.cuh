@@ -3,8 +3,6 @@
 
 #include <cuda.h>
 
-#include <atomic>
-
 #include "int8.cuh"
 
 namespace paro {
@@ -18,9 +16,6 @@ cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream
 bool w8_map(CUtensorMap* map, const int8_t* p, int rows, int d_in, int box_rows);
 // Tensor map of 16-bit y [rows][d_out], d_out a multiple of 8: boxes of 32 x 32, 64-byte swizzle.
 bool w8_out_map(CUtensorMap* map, const uint16_t* y, int rows, int d_out);
-// Allows a kernel up to `bytes` of dynamic shared memory on the current device,
-// once for each device (`done` has a bit for each, and is the kernel's own).
-cudaError_t w8_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 
 __device__ __forceinline__ float w8a8_scaled(int acc, float sx, float sw) {
   return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);

@@ -29,9 +29,9 @@ namespace {
 using namespace ptx;
 
 constexpr int kRows = 128, kK = 128, kThreads = 192;
-constexpr int kMaxSmem = 130 * 1024;  // a CTA's ring, or its sums for 128 tokens of a gated pair
+constexpr int kMaxSmem = 105 * 1024;  // a CTA's ring, or its sums
 constexpr int kMaxStages = 8, kMaxSplit = 8;  // 8: the portable size of a cluster
-constexpr int kAhead = 32;  // stages asked for in L2 before the kernel before is done
+constexpr int kAhead = 4;  // stages asked for in L2 before the kernel before is done
 
 struct FewArgs {
   CUtensorMap w, w2, q;
@@ -41,7 +41,7 @@ struct FewArgs {
   const uint16_t* bias;
   uint16_t* y;
   int M, d_out, blocks;  // blocks: of 128 columns of d_in
-  int split, stages;
+  int split, stages, xrows;  // xrows: tokens a copy brings, at most TN
 };
 
 template <int TN, bool GATED>
@@ -118,7 +118,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
         if (aborted()) break;
         const uint32_t dst = ring + s * Geo::STAGE, bar = b_full + 8 * s;
         const int x = (k0 + i) * kK;
-        mbar_expect_tx(bar, Geo::STAGE);
+        mbar_expect_tx(bar, (NW * kRows + A.xrows) * kK);
         tma_load(dst, &A.w, x, n0, bar);
         if constexpr (GATED) tma_load(dst + kRows * kK, &A.w2, x, n0, bar);
         tma_load(dst + NW * kRows * kK, &A.q, x, m0, bar);
@@ -269,12 +269,15 @@ template <int TN, bool GATED, bool F16>
 cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
   using Geo = FewGeo<TN, GATED>;
   const int tiles = (A.d_out + kRows - 1) / kRows, mtiles = (A.M + TN - 1) / TN;
-  const int sms = device_sm_count();
+  // As many shares of d_in as still leave every CTA resident at once, two on an
+  // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
+  const int places = 2 * device_sm_count();
+  auto fits = [&](int n) { return tiles * mtiles * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };
   int split = 1;
-  while (split < kMaxSplit && tiles * mtiles * split * 2 <= 2 * sms && 2 * split <= A.blocks) split *= 2;
+  while (split < kMaxSplit && fits(2 * split) && 2 * split <= A.blocks) split *= 2;
   A.split = split;
   const int per = (A.blocks + split - 1) / split;
-  constexpr int kBudget = 100 * 1024;
+  constexpr int kBudget = 104 * 1024;  // of 228 KB, for two CTAs
   int stages = kBudget / Geo::STAGE;
   if (stages < 2) stages = 2;
   if (stages > kMaxStages) stages = kMaxStages;
@@ -285,7 +288,7 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
   bytes += 1024;
   auto kernel = w8a8_few_kernel<TN, GATED, F16>;
   static std::atomic<uint64_t> limit{0};
-  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kMaxSmem, limit);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem, limit);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(tiles * split, mtiles);
@@ -306,8 +309,12 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
 
 template <int TN>
 cudaError_t launch_tn(const W8a8Args& a, FewArgs& A, int* status, cudaStream_t s) {
-  if (!w8_map(&A.q, a.q, a.M, a.d_in, TN)) return cudaErrorInvalidValue;
-  if (a.w2) return a.f16 ? launch_few<TN, true, true>(A, status, s) : launch_few<TN, true, false>(A, status, s);
+  // rows of the last tile's box behind the last token are zeros; where M < TN the
+  // columns behind it multiply what lies there, unread
+  A.xrows = a.M < TN ? a.M : TN;
+  if (!w8_map(&A.q, a.q, a.M, a.d_in, A.xrows)) return cudaErrorInvalidValue;
+  if constexpr (TN <= 64)
+    if (a.w2) return a.f16 ? launch_few<TN, true, true>(A, status, s) : launch_few<TN, true, false>(A, status, s);
   return a.f16 ? launch_few<TN, false, true>(A, status, s) : launch_few<TN, false, false>(A, status, s);
 }
 
@@ -327,7 +334,8 @@ cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream)
   A.blocks = (a.d_in + kK - 1) / kK;
   if (a.M <= 16) return launch_tn<16>(a, A, status, stream);
   if (a.M <= 32) return launch_tn<32>(a, A, status, stream);
-  if (a.M <= 64) return launch_tn<64>(a, A, status, stream);
+  // a gated pair's sums for 128 tokens would leave room for one CTA on an SM
+  if (a.M <= 64 || a.w2) return launch_tn<64>(a, A, status, stream);
   return launch_tn<128>(a, A, status, stream);
 }
 

@@ -262,7 +262,7 @@ template <bool GATED, bool F16>
 cudaError_t launch_many(const ManyArgs& A, int* status, cudaStream_t s) {
   auto kernel = w8a8_many_kernel<GATED, F16>;
   static std::atomic<uint64_t> limit{0};
-  const cudaError_t e = w8_smem_limit(reinterpret_cast<const void*>(kernel), kSmem, limit);
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kSmem, limit);
   if (e != cudaSuccess) return e;
   const int pairs = device_sm_count() / 2;
   cudaLaunchConfig_t cfg = {};
