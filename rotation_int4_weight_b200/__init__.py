@@ -92,12 +92,23 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+try:
+    from . import _binding
+except ImportError as e:
+    raise ImportError("the _binding module is missing or not built for this Python: build it with "
+                      "`python rotation_int4_weight_b200/_build.py`") from e
+
 
 def _check(status: int, what: str) -> None:
     if status != 0:
         name = lib.paro_status_string(status).decode()
         msg = lib.paro_last_error().decode()
         raise ParoError(status, f"{what}: {name}: {msg}")
+
+
+_binding.setup(torch, _check, tuple(ctypes.cast(getattr(lib, n), _P).value for n in (
+    "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
+    "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear")))
 
 
 def _ptr(t: torch.Tensor | None):
@@ -254,78 +265,24 @@ def paro_rotate_w4a4_linear(x: torch.Tensor, pairs, cos_t, sin_t, scale, qweight
     return out
 
 
-# ---- 8-bit path: the tensors' types, shapes and devices are checked here, since the
-# C ABI sees addresses only
-_ACT = {torch.bfloat16: 0, torch.float16: 1}  # paro_dtype
-
-
-def _act(dtype) -> int:
-    code = _ACT.get(dtype)
-    if code is None:
-        raise ValueError(f"expected bfloat16 or float16, got {dtype}")
-    return code
-
-
-def _rows(t: torch.Tensor, name: str):
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have two dimensions, got {tuple(t.shape)}")
-    return t.shape
-
-
-def _arg(t: torch.Tensor | None, dtype, shape, dev: int, name: str):
-    """Address of a tensor (None: NULL) after a check of its type, shape, layout and device."""
-    if t is None:
-        return None
-    if t.dtype is not dtype or t.shape != shape:
-        raise ValueError(f"{name}: expected {dtype} {tuple(shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.get_device() != dev or dev < 0:
-        raise ValueError(f"{name}: expected a tensor of the same CUDA device as the first one, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous tensor")
-    return t.data_ptr()
-
-
-def _launch(fn, what: str, dev: int, stream, *args):
-    """fn(*args, stream) with `dev` current, on its current stream or the one given."""
-    if stream is None:
-        handle = torch._C._cuda_getCurrentRawStream(dev)
-    elif stream.device.index == dev:
-        handle = stream.cuda_stream
-    else:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{dev}")
-    if torch._C._cuda_getDevice() == dev:
-        st = fn(*args, handle)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, handle)
-    if st != 0:
-        _check(st, what)
-
-
-def _new(stream, dtype, device, *shape):
-    """A new tensor that belongs to the stream it is first used on."""
-    if stream is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(*shape, dtype=dtype, device=device)
+# ---- 8-bit path: module _binding (csrc/binding.cpp) checks the tensors' types, shapes,
+# layouts and devices, allocates the outputs and calls the library
+def _elsewhere(fn, stream, first: torch.Tensor, *args):
+    """fn(first, *args) on the stream given, or with the tensors' device current."""
+    dev = first.get_device()
+    if stream is not None and stream.device.index != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {first.device}")
+    with torch.cuda.device(dev) if stream is None else torch.cuda.stream(stream):
+        return fn(first, *args)
 
 
 def paro_quantize_activations_int8(x: torch.Tensor, *, q=None, sx=None, stream=None):
     """Row codes of x [M, d] (bf16 or fp16): (q int8 [M, d] in -127..127, sx fp32 [M]); a code stands for q * sx."""
-    M, d = _rows(x, "x")
-    t, dev = x.dtype, x.get_device()
-    code, px = _act(t), _arg(x, t, x.shape, dev, "x")
-    if q is None:
-        q = _new(stream, torch.int8, x.device, M, d)
-    else:
-        _arg(q, torch.int8, (M, d), dev, "q")
-    if sx is None:
-        sx = _new(stream, torch.float32, x.device, M)
-    else:
-        _arg(sx, torch.float32, (M,), dev, "sx")
-    _launch(lib.paro_quantize_activations_int8, "paro_quantize_activations_int8", dev, stream, px, q.data_ptr(),
-            sx.data_ptr(), M, d, code)
-    return q, sx
+    if stream is None:
+        r = _binding.quantize(x, q, sx)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.quantize, stream, x, q, sx)
 
 
 def paro_rms_norm_int8(x: torch.Tensor, gain=None, residual=None, *, eps: float = 1e-6, hidden=None, q=None, sx=None,
@@ -335,104 +292,43 @@ def paro_rms_norm_int8(x: torch.Tensor, gain=None, residual=None, *, eps: float 
     Returns (q int8 [M, d], sx fp32 [M], hidden [M, d]); hidden is h in x's type (it may be given,
     and may be x or residual), or None without a residual.
     """
-    M, d = _rows(x, "x")
-    if residual is None and hidden is not None:
-        raise ValueError("hidden is written only with a residual")
-    t, dev = x.dtype, x.get_device()
-    code, px = _act(t), _arg(x, t, x.shape, dev, "x")
-    pr, pg = _arg(residual, t, x.shape, dev, "residual"), _arg(gain, t, (d,), dev, "gain")
-    if residual is not None:
-        if hidden is None:
-            hidden = _new(stream, t, x.device, M, d)
-        else:
-            _arg(hidden, t, x.shape, dev, "hidden")
-    if q is None:
-        q = _new(stream, torch.int8, x.device, M, d)
-    else:
-        _arg(q, torch.int8, (M, d), dev, "q")
-    if sx is None:
-        sx = _new(stream, torch.float32, x.device, M)
-    else:
-        _arg(sx, torch.float32, (M,), dev, "sx")
-    _launch(lib.paro_rms_norm_int8, "paro_rms_norm_int8", dev, stream, px, pr, pg, eps,
-            None if hidden is None else hidden.data_ptr(), q.data_ptr(), sx.data_ptr(), M, d, code)
-    return q, sx, hidden
-
-
-def _tables8(pairs, cos_t, sin_t, scale, d, dev):
-    """(K, pairs, cos, sin, scale) of a transform of width d as the 8-bit calls pass it."""
-    K = _K(pairs)
-    if K and (cos_t is None or sin_t is None):
-        raise ValueError("pairs need cos_t and sin_t")
-    if pairs is not None and pairs.dtype not in (torch.int16, torch.uint16):
-        raise ValueError(f"pairs: expected int16 or uint16, got {pairs.dtype}")
-    return (K, _arg(pairs, pairs.dtype if K else None, (K, d // 2, 2), dev, "pairs") if K else None,
-            _arg(cos_t, torch.float32, (K, d // 2), dev, "cos_t") if K else None,
-            _arg(sin_t, torch.float32, (K, d // 2), dev, "sin_t") if K else None,
-            _arg(scale, torch.float32, (d,), dev, "scale"))
+    if stream is None:
+        r = _binding.norm(x, gain, residual, eps, hidden, q, sx)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.norm, stream, x, gain, residual, eps, hidden, q, sx)
 
 
 def paro_pack_weights_int8(W: torch.Tensor, pairs=None, cos_t=None, sin_t=None, scale=None, *, workspace=None,
                            qweight=None, wscales=None, stream=None):
     """Fold the layer's transform into fp32 W [d_out, d_in] and take its row codes:
     (qweight int8 [d_out, d_in], wscales fp32 [d_out])."""
-    d_out, d_in = _rows(W, "W")
-    dev = W.get_device()
-    pw = _arg(W, torch.float32, W.shape, dev, "W")
-    tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
-    if qweight is None:
-        qweight = _new(stream, torch.int8, W.device, d_out, d_in)
-    if wscales is None:
-        wscales = _new(stream, torch.float32, W.device, d_out)
-    if tables[0] == 0 and scale is None:
-        workspace = None
-    elif workspace is None:
-        workspace = _new(stream, torch.float32, W.device, d_out, d_in)
-    _launch(lib.paro_pack_weights_int8, "paro_pack_weights_int8", dev, stream, pw, d_out, d_in, *tables,
-            _arg(workspace, torch.float32, (d_out, d_in), dev, "workspace"),
-            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
-            _arg(wscales, torch.float32, (d_out,), dev, "wscales"))
-    return qweight, wscales
+    if stream is None:
+        r = _binding.pack(W, pairs, cos_t, sin_t, scale, workspace, qweight, wscales)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.pack, stream, W, pairs, cos_t, sin_t, scale, workspace, qweight, wscales)
 
 
 def paro_w8a8_linear(q: torch.Tensor, sx, qweight, wscales, bias=None, *, out=None, out_dtype=torch.bfloat16,
                      stream=None):
     """int8 linear on codes q [M, d_in] and scales sx [M]: y = sx wscales (q qweight^T) + bias, [M, d_out] in
     out's type or out_dtype (bf16 or fp16)."""
-    M, d_in = _rows(q, "q")
-    d_out, dev = _rows(qweight, "qweight")[0], q.get_device()
-    t = out_dtype if out is None else out.dtype
-    code = _act(t)
-    pq = _arg(q, torch.int8, q.shape, dev, "q")
-    if out is None:
-        out = _new(stream, t, q.device, M, d_out)
-    else:
-        _arg(out, t, (M, d_out), dev, "out")
-    _launch(lib.paro_w8a8_linear, "paro_w8a8_linear", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
-            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
-            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, t, (d_out,), dev, "bias"), out.data_ptr(),
-            M, d_in, d_out, code)
-    return out
+    if stream is None:
+        r = _binding.linear(q, sx, qweight, wscales, bias, out, out_dtype)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.linear, stream, q, sx, qweight, wscales, bias, out, out_dtype)
 
 
 def paro_w8a8_swiglu(q: torch.Tensor, sx, gate_qweight, gate_wscales, up_qweight, up_wscales, *, out=None,
                      out_dtype=torch.bfloat16, stream=None):
     """Gated pair of int8 linears in one kernel: silu(gate) * up, [M, d_out] in out's type or out_dtype."""
-    M, d_in = _rows(q, "q")
-    d_out, dev = _rows(gate_qweight, "gate_qweight")[0], q.get_device()
-    t = out_dtype if out is None else out.dtype
-    code = _act(t)
-    pq = _arg(q, torch.int8, q.shape, dev, "q")
-    if out is None:
-        out = _new(stream, t, q.device, M, d_out)
-    else:
-        _arg(out, t, (M, d_out), dev, "out")
-    _launch(lib.paro_w8a8_swiglu, "paro_w8a8_swiglu", dev, stream, pq, _arg(sx, torch.float32, (M,), dev, "sx"),
-            _arg(gate_qweight, torch.int8, (d_out, d_in), dev, "gate_qweight"),
-            _arg(gate_wscales, torch.float32, (d_out,), dev, "gate_wscales"),
-            _arg(up_qweight, torch.int8, (d_out, d_in), dev, "up_qweight"),
-            _arg(up_wscales, torch.float32, (d_out,), dev, "up_wscales"), out.data_ptr(), M, d_in, d_out, code)
-    return out
+    if stream is None:
+        r = _binding.swiglu(q, sx, gate_qweight, gate_wscales, up_qweight, up_wscales, out, out_dtype)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.swiglu, stream, q, sx, gate_qweight, gate_wscales, up_qweight, up_wscales, out, out_dtype)
 
 
 def paro_rotate_w8a8_workspace_bytes(M: int, d_in: int) -> int:
@@ -442,20 +338,12 @@ def paro_rotate_w8a8_workspace_bytes(M: int, d_in: int) -> int:
 def paro_rotate_w8a8_linear(x: torch.Tensor, pairs, cos_t, sin_t, scale, qweight, wscales, bias=None, *, out=None,
                             workspace=None, stream=None):
     """The 8-bit path of one linear: transform, row codes, int8 linear; bf16 [M, d_in] -> bf16 [M, d_out]."""
-    M, d_in = _rows(x, "x")
-    d_out, dev = _rows(qweight, "qweight")[0], x.get_device()
-    px = _arg(x, torch.bfloat16, x.shape, dev, "x")
-    tables = _tables8(pairs, cos_t, sin_t, scale, d_in, dev)
-    if out is None:
-        out = _new(stream, torch.bfloat16, x.device, M, d_out)
-    if workspace is None:
-        workspace = _new(stream, torch.uint8, x.device, max(paro_rotate_w8a8_workspace_bytes(M, d_in), 256))
-    _launch(lib.paro_rotate_w8a8_linear, "paro_rotate_w8a8_linear", dev, stream, px, *tables,
-            _arg(qweight, torch.int8, (d_out, d_in), dev, "qweight"),
-            _arg(wscales, torch.float32, (d_out,), dev, "wscales"), _arg(bias, torch.bfloat16, (d_out,), dev, "bias"),
-            _arg(out, torch.bfloat16, (M, d_out), dev, "out"), M, d_in, d_out,
-            _arg(workspace, torch.uint8, workspace.shape, dev, "workspace"), workspace.numel())
-    return out
+    if stream is None:
+        r = _binding.rotate_linear(x, pairs, cos_t, sin_t, scale, qweight, wscales, bias, out, workspace)
+        if r is not NotImplemented:
+            return r
+    return _elsewhere(_binding.rotate_linear, stream, x, pairs, cos_t, sin_t, scale, qweight, wscales, bias, out,
+                      workspace)
 
 
 def paro_w4_linear(x: torch.Tensor, qweight, scales, zeros, *, out=None, group_size: int = 128, stream=None):

@@ -1,4 +1,5 @@
-"""Builds libparo.so (the C-ABI library) in-tree with nvcc for sm_100a.
+"""Builds libparo.so (the C-ABI library) in-tree with nvcc for sm_100a, and _binding.so,
+the 8-bit calls' Python module, with the host compiler.
 
 Usage: python rotation_int4_weight_b200/_build.py [--force] [-v] [--timeline]
 (run it as a file: importing the package would first load the library it builds)
@@ -15,12 +16,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libparo.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD_TIMELINE = os.path.join(PKG, "_build_timeline")
 LIB_TIMELINE = os.path.join(PKG, "libparo_timeline.so")
 
@@ -47,6 +50,18 @@ def _newer(target: str, deps: list[str]) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """The 8-bit calls' Python module: host code only, against Python's headers."""
+    src = os.path.join(CSRC, "binding.cpp")
+    if force or not _newer(BINDING, [src, os.path.join(ROOT, "include", "paro.h")]):
+        cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
+               "-fvisibility=hidden", "-Wall", "-I", sysconfig.get_paths()["include"], src, "-o", BINDING]
+        if verbose:
+            print(" ".join(cmd), flush=True)
+        subprocess.run(cmd, check=True)
+    return BINDING
+
+
 def build(force: bool = False, verbose: bool = False, timeline: bool = False) -> str:
     build_dir, lib = (BUILD_TIMELINE, LIB_TIMELINE) if timeline else (BUILD, LIB)
     defines = ["-DPARO_TIMELINE=1"] if timeline else []
@@ -70,6 +85,7 @@ def build(force: bool = False, verbose: bool = False, timeline: bool = False) ->
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)
+    build_binding(force, verbose)
     return lib
 
 
