@@ -840,10 +840,14 @@ paro_status check_w8_weights(const int8_t* w, const float* s) {
   return PARO_OK;
 }
 
+constexpr int kMaxW8Rows = 1 << 30;  // tile coordinates stay within 31 bits
+
 // Checks and launches both int8 linears (d_w2 and d_s2 null: the plain one).
 paro_status run_w8a8(const int8_t* d_q, const float* d_sx, const int8_t* d_w, const float* d_s, const int8_t* d_w2,
                      const float* d_s2, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in, int d_out,
                      paro_dtype dtype, paro_stream_t stream) {
+  if (M > kMaxW8Rows || d_out > kMaxW8Rows)
+    return fail(PARO_ERR_UNSUPPORTED, "M = %d or d_out = %d exceeds %d", M, d_out, kMaxW8Rows);
   if (!d_q || !d_sx || !d_y) return fail(PARO_ERR_INVALID_ARG, "null activation pointer");
   if (!aligned(d_q, 16) || !aligned(d_sx, 4) || !aligned(d_y, 16))
     return fail(PARO_ERR_INVALID_ARG, "q and y must be 16-byte aligned, sx 4-byte");

@@ -7,6 +7,13 @@
 
 namespace paro {
 
+// How the kernel for few tokens cuts a call: tiles of 128 channels, mtiles of
+// `tokens` tokens, and each tile's d_in into `split` shares.
+struct W8a8Few {
+  int tokens, tiles, mtiles, split;
+};
+W8a8Few w8a8_few_shape(const W8a8Args& a);
+
 // The two kernels of launch_w8a8.
 cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream);
 cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream);

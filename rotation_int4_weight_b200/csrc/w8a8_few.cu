@@ -8,10 +8,15 @@
 //             tokens' TN x 128 bytes (128-byte swizzle) into a ring of stages;
 //   warp 1    MMA: four tcgen05.mma kind::i8 (128 x TN x 32) a stage, into 32-bit
 //             sums in tensor memory;
-//   warps 2-5 epilogue: the sums go to the CTA's own shared memory (the ring is
-//             done by then), and after a cluster barrier each CTA adds up and
-//             writes its part of the tokens from all the others': a warp takes a
-//             token, a lane four channels, the loads of all shares at once.
+//   warps 2-5 epilogue: thread = channel.  Token t of a tile belongs to CTA t mod
+//             the cluster's size, which adds up all shares' sums for it and
+//             writes y (a warp takes a token, a lane four channels).  Up to 32
+//             tokens, every CTA stores its sums into the owners' shared memory,
+//             beside their rings, and ends; more stay in the CTA's own, where the
+//             ring was, for the owners to read between two cluster barriers.
+//             Measured, stored / read, us: 16 tokens gated 1536 -> 8960 9.3 /
+//             10.2, 1 token 1536 -> 1536 3.7 / 4.2; 64 tokens 4096 -> 4096 11.0 /
+//             9.6, 128 tokens 14.0 / 11.8.
 // Whole sums: the order of the shares does not matter, there is no workspace and
 // nothing to reset between calls.
 //
@@ -48,7 +53,8 @@ template <int TN, bool GATED>
 struct FewGeo {
   static constexpr int NW = GATED ? 2 : 1;
   static constexpr int STAGE = NW * kRows * kK + TN * kK;
-  static constexpr int SUMS = TN * NW * kRows * 4;  // a CTA's sums for the others
+  static constexpr int SUMS = TN * NW * kRows * 4;  // the sums that a CTA holds
+  static constexpr bool STORED = TN <= 32;          // ... of its own tokens, beside the ring
   static constexpr int COLS = NW * TN < 32 ? 32 : NW * TN;
 };
 
@@ -58,7 +64,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   using Geo = FewGeo<TN, GATED>;
   constexpr int NW = Geo::NW;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 1];
+  __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, s_issued, s_committed;
   __shared__ float s_sx[TN];
@@ -66,7 +72,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_u32(smem);
   const uint32_t b_full = smem_u32(&bars[0]), b_empty = smem_u32(&bars[kMaxStages]);
-  const uint32_t b_acc = smem_u32(&bars[2 * kMaxStages]);
+  const uint32_t b_acc = smem_u32(&bars[2 * kMaxStages]), b_sums = smem_u32(&bars[2 * kMaxStages + 1]);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = A.split, stages = A.stages;
   const int rank = split > 1 ? (int)cluster_rank() : 0;
@@ -83,6 +89,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
       mbar_init(b_empty + 8 * s, 1);
     }
     mbar_init(b_acc, 1);
+    mbar_init(b_sums, 4 * split);  // the epilogue warps of all shares
     abort_flag = 0;
     s_issued = 0;
     s_committed = 0;
@@ -93,6 +100,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
+  cluster_arrive();  // (the wait comes before the first store to another CTA)
   grid_trigger();
   if (warp == 0 && lane == 0) {
     for (int i = 0; i < nk && i < kAhead; ++i) {
@@ -157,6 +165,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   float sw[NW][4], bias[4];
   if (warp >= 2) {
     for (int t = threadIdx.x - 64; t < tokens; t += kRows) s_sx[t] = A.sx[m0 + t];
+    asm volatile("bar.sync 1, 128;\n" ::: "memory");
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const bool in = n + e < A.d_out;
@@ -164,83 +173,113 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
       if constexpr (GATED) sw[NW - 1][e] = in ? A.sw2[n + e] : 0.0f;
       bias[e] = !GATED && A.bias && in ? from_16<F16>(A.bias[n + e]) : 0.0f;
     }
-    if (mbar_wait(b_acc, 0)) {
-      tc_fence_after();
-      const int quarter = warp & 3, ch = quarter * 32 + lane;  // the tensor memory lanes this warp may read
-      const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-      int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
-#pragma unroll 1
-      for (int c0 = 0; c0 < tokens; c0 += 16) {
-        int v[NW][16];
-#pragma unroll
-        for (int g = 0; g < NW; ++g) tmem_ld(lanes + g * TN + c0, v[g]);
-        tmem_ld_wait();
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          if (c0 + c < tokens)
-#pragma unroll
-            for (int g = 0; g < NW; ++g) sums[((c0 + c) * NW + g) * kRows + ch] = v[g][c];
-      }
-    } else {
-      fail();
-    }
   }
-  // the sums of all shares are there; a CTA whose wait gave up has none, and
-  // nobody of its cluster writes then
-  __syncwarp();
-  if (split > 1) {
+  const int quarter = warp & 3, ch = quarter * 32 + lane;  // the tensor memory lanes this warp may read
+  const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
+  // put(t, g, sum) of this thread's channel for every token and weight matrix
+  auto drain = [&](auto put) {
+    tc_fence_after();
+#pragma unroll 1
+    for (int c0 = 0; c0 < tokens; c0 += 16) {
+      int v[NW][16];
+#pragma unroll
+      for (int g = 0; g < NW; ++g) tmem_ld(lanes + g * TN + c0, v[g]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (c0 + c < tokens)
+#pragma unroll
+          for (int g = 0; g < NW; ++g) put(c0 + c, g, v[g][c]);
+    }
+  };
+  // y of token t for this lane's four channels from get(share, g)
+  auto finish = [&](int t, auto get) {
+    int4 part[NW][kMaxSplit];
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+      if (r < split)
+#pragma unroll
+        for (int g = 0; g < NW; ++g) part[g][r] = get(r, g);
+    int sum[NW][4] = {};
+#pragma unroll
+    for (int r = 0; r < kMaxSplit; ++r)
+      if (r < split)
+#pragma unroll
+        for (int g = 0; g < NW; ++g) {
+          sum[g][0] += part[g][r].x;
+          sum[g][1] += part[g][r].y;
+          sum[g][2] += part[g][r].z;
+          sum[g][3] += part[g][r].w;
+        }
+    const float sx = s_sx[t];
+    uint32_t o[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float v = w8a8_scaled(sum[0][e], sx, sw[0][e]);
+      if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1][e], sx, sw[NW - 1][e]));
+      else v += bias[e];
+      o[e] = to_16<F16>(v);
+    }
+    uint16_t* dst = A.y + (size_t)(m0 + t) * A.d_out + n;
+    if ((A.d_out & 3) == 0) {
+      if (n < A.d_out) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (n + e < A.d_out) dst[e] = (uint16_t)o[e];
+    }
+  };
+
+  if constexpr (Geo::STORED) {
+    cluster_wait();  // all barriers of the cluster are there
+    if (warp >= 2) {
+      // [share][its slot of the owner's tokens][NW][128]
+      const uint32_t sums = ring + stages * Geo::STAGE;
+      const int shift = 31 - __clz(split), slots = (tokens + split - 1) >> shift;  // split: a power of two
+      const bool good = mbar_wait(b_acc, 0);
+      if (good) {
+        drain([&](int t, int g, int v) {
+          const int slot = t >> shift, owner = t & (split - 1);
+          st_cluster(mapa(sums + (((rank * slots + slot) * NW + g) * kRows + ch) * 4, owner), v);
+        });
+        __syncwarp();
+        if (lane < split && lane < tokens) mbar_arrive_cluster(mapa(b_sums, lane));
+      } else {
+        fail();
+      }
+      if (rank < tokens) {
+        if (good && mbar_wait(b_sums, 0)) {
+          const int4* from = reinterpret_cast<const int4*>(smem + stages * Geo::STAGE) + lane;
+#pragma unroll 2
+          for (int t = rank + split * (warp - 2); t < tokens; t += split * 4)
+            finish(t, [&](int r, int g) { return from[((r * slots + (t >> shift)) * NW + g) * (kRows / 4)]; });
+        } else {
+          fail();
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    if (warp >= 2) {
+      int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
+      if (mbar_wait(b_acc, 0)) drain([&](int t, int g, int v) { sums[(t * NW + g) * kRows + ch] = v; });
+      else fail();
+    }
+    // a CTA whose wait gave up has no sums: nobody of its cluster writes then
+    __syncwarp();
+    cluster_wait();
     cluster_arrive();
     cluster_wait();
-  } else {
-    __syncthreads();
-  }
-  if (warp >= 2) {
-    const uint32_t flag = smem_u32(&abort_flag);
-    if (__all_sync(0xffffffffu, lane >= split || ld_cluster(mapa(flag, lane)) == 0)) {
-      const uint32_t mine = ring + lane * 16;
+    if (warp >= 2) {
+      const uint32_t flag = smem_u32(&abort_flag);
+      if (__all_sync(0xffffffffu, lane >= split || ld_cluster(mapa(flag, lane)) == 0)) {
+        const uint32_t mine = ring + lane * 16;
 #pragma unroll 2
-      for (int t = rank + split * (warp - 2); t < tokens; t += split * 4) {
-        int4 part[NW][kMaxSplit];
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split) {
-            const uint32_t at = mapa(mine + t * (NW * kRows * 4), r);
-#pragma unroll
-            for (int g = 0; g < NW; ++g) part[g][r] = ld_cluster4(at + g * kRows * 4);
-          }
-        int sum[NW][4] = {};
-#pragma unroll
-        for (int r = 0; r < kMaxSplit; ++r)
-          if (r < split)
-#pragma unroll
-            for (int g = 0; g < NW; ++g) {
-              sum[g][0] += part[g][r].x;
-              sum[g][1] += part[g][r].y;
-              sum[g][2] += part[g][r].z;
-              sum[g][3] += part[g][r].w;
-            }
-        const float sx = s_sx[t];
-        uint32_t o[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = w8a8_scaled(sum[0][e], sx, sw[0][e]);
-          if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1][e], sx, sw[NW - 1][e]));
-          else v += bias[e];
-          o[e] = to_16<F16>(v);
-        }
-        uint16_t* dst = A.y + (size_t)(m0 + t) * A.d_out + n;
-        if ((A.d_out & 3) == 0) {
-          if (n < A.d_out) *reinterpret_cast<uint2*>(dst) = make_uint2(o[0] | (o[1] << 16), o[2] | (o[3] << 16));
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (n + e < A.d_out) dst[e] = (uint16_t)o[e];
-        }
+        for (int t = rank + split * (warp - 2); t < tokens; t += split * 4)
+          finish(t, [&](int r, int g) { return ld_cluster4(mapa(mine + (t * NW + g) * (kRows * 4), r)); });
       }
     }
-  }
-  __syncwarp();
-  if (split > 1) {
+    __syncwarp();
     cluster_arrive();  // the others' sums are read: their CTAs may end
     cluster_wait();
   }
@@ -263,27 +302,25 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     tc_fence_after();
     tmem_dealloc<1>(tmem, Geo::COLS);
   }
+  if (abort_flag) {  // a CTA that gave up outlives what others may still store to it (or they have ended)
+    cluster_arrive();
+    cluster_wait();
+  }
 }
 
 template <int TN, bool GATED, bool F16>
-cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
+cudaError_t launch_few(FewArgs& A, const W8a8Few& f, int* status, cudaStream_t stream) {
   using Geo = FewGeo<TN, GATED>;
-  const int tiles = (A.d_out + kRows - 1) / kRows, mtiles = (A.M + TN - 1) / TN;
-  // As many shares of d_in as still leave every CTA resident at once, two on an
-  // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
-  const int places = 2 * device_sm_count();
-  auto fits = [&](int n) { return tiles * mtiles * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };
-  int split = 1;
-  while (split < kMaxSplit && fits(2 * split) && 2 * split <= A.blocks) split *= 2;
-  A.split = split;
-  const int per = (A.blocks + split - 1) / split;
+  const int per = (A.blocks + f.split - 1) / f.split;
+  A.split = f.split;
   constexpr int kBudget = 104 * 1024;  // of 228 KB, for two CTAs
-  int stages = kBudget / Geo::STAGE;
+  int stages = (kBudget - (Geo::STORED ? Geo::SUMS : 0)) / Geo::STAGE;
   if (stages < 2) stages = 2;
   if (stages > kMaxStages) stages = kMaxStages;
   if (stages > per) stages = per;
   int bytes = stages * Geo::STAGE;
-  if (bytes < Geo::SUMS) bytes = Geo::SUMS;
+  if (Geo::STORED) bytes += Geo::SUMS;
+  else if (bytes < Geo::SUMS) bytes = Geo::SUMS;
   A.stages = stages;
   bytes += 1024;
   auto kernel = w8a8_few_kernel<TN, GATED, F16>;
@@ -291,13 +328,13 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem, limit);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(tiles * split, mtiles);
+  cfg.gridDim = dim3(f.tiles * f.split, f.mtiles);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = split;
+  at[0].val.clusterDim.x = f.split;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -308,17 +345,37 @@ cudaError_t launch_few(FewArgs& A, int* status, cudaStream_t stream) {
 }
 
 template <int TN>
-cudaError_t launch_tn(const W8a8Args& a, FewArgs& A, int* status, cudaStream_t s) {
+cudaError_t launch_tn(const W8a8Args& a, FewArgs& A, const W8a8Few& f, int* status, cudaStream_t s) {
   // rows of the last tile's box behind the last token are zeros; where M < TN the
   // columns behind it multiply what lies there, unread
   A.xrows = a.M < TN ? a.M : TN;
   if (!w8_map(&A.q, a.q, a.M, a.d_in, A.xrows)) return cudaErrorInvalidValue;
   if constexpr (TN <= 64)
-    if (a.w2) return a.f16 ? launch_few<TN, true, true>(A, status, s) : launch_few<TN, true, false>(A, status, s);
-  return a.f16 ? launch_few<TN, false, true>(A, status, s) : launch_few<TN, false, false>(A, status, s);
+    if (a.w2) return a.f16 ? launch_few<TN, true, true>(A, f, status, s) : launch_few<TN, true, false>(A, f, status, s);
+  return a.f16 ? launch_few<TN, false, true>(A, f, status, s) : launch_few<TN, false, false>(A, f, status, s);
 }
 
 }  // namespace
+
+W8a8Few w8a8_few_shape(const W8a8Args& a) {
+  W8a8Few f;
+  // a gated pair's sums for 128 tokens would leave room for one CTA on an SM
+  f.tokens = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || a.w2 ? 64 : 128;
+  f.tiles = (a.d_out + kRows - 1) / kRows;
+  f.mtiles = (a.M + f.tokens - 1) / f.tokens;
+  // As many shares of d_in as still leave every CTA resident at once, two on an
+  // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
+  // One SM draws at most about 40 GB/s through TMA from HBM, so more CTAs pay up
+  // to there: 14336 -> 4096 at one token takes 49.5, 27.4, 16.8, 13.9 us with 1,
+  // 2, 4, 8 shares; tiles of fewer rows that even out the SMs' bytes won 4% at
+  // most, and lost it elsewhere.
+  const long long places = 2 * device_sm_count(), ctas = (long long)f.tiles * f.mtiles;
+  auto fits = [&](int n) { return ctas * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };
+  const int blocks = (a.d_in + kK - 1) / kK;
+  f.split = 1;
+  while (f.split < kMaxSplit && fits(2 * f.split) && 2 * f.split <= blocks) f.split *= 2;
+  return f;
+}
 
 cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream) {
   FewArgs A;
@@ -332,11 +389,13 @@ cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream)
   A.M = a.M;
   A.d_out = a.d_out;
   A.blocks = (a.d_in + kK - 1) / kK;
-  if (a.M <= 16) return launch_tn<16>(a, A, status, stream);
-  if (a.M <= 32) return launch_tn<32>(a, A, status, stream);
-  // a gated pair's sums for 128 tokens would leave room for one CTA on an SM
-  if (a.M <= 64 || a.w2) return launch_tn<64>(a, A, status, stream);
-  return launch_tn<128>(a, A, status, stream);
+  const W8a8Few f = w8a8_few_shape(a);
+  switch (f.tokens) {
+    case 16: return launch_tn<16>(a, A, f, status, stream);
+    case 32: return launch_tn<32>(a, A, f, status, stream);
+    case 64: return launch_tn<64>(a, A, f, status, stream);
+    default: return launch_tn<128>(a, A, f, status, stream);
+  }
 }
 
 }  // namespace paro
