@@ -8,14 +8,16 @@
 namespace paro {
 
 // How the kernel for few tokens cuts a call: tiles of 128 channels, mtiles of
-// `tokens` tokens, and each tile's d_in into `split` shares.
+// `tokens` tokens, and each tile's d_in into `split` shares.  An estimate of
+// LLONG_MAX: it does not take the call.
 struct W8a8Few {
   int tokens, tiles, mtiles, split;
+  long long ns;  // estimate of the call's time
 };
 W8a8Few w8a8_few_shape(const W8a8Args& a);
 
 // The two kernels of launch_w8a8.
-cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream);
+cudaError_t launch_w8a8_few(const W8a8Args& a, const W8a8Few& f, int* status, cudaStream_t stream);
 cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream);
 
 // Tensor map of int8 [rows][d_in]: boxes of 128 columns x box_rows, 128-byte

@@ -23,6 +23,8 @@
 // The launch overlaps the kernel before it: until that one is done a CTA sets up
 // its barriers and asks for its weights in L2 only, which is right whoever wrote
 // them last; every read and write of its own comes after the wait.
+#include <climits>
+
 #include "int8.cuh"
 #include "tc_ptx.cuh"
 #include "w4_stream.cuh"  // device_sm_count
@@ -358,26 +360,57 @@ cudaError_t launch_tn(const W8a8Args& a, FewArgs& A, const W8a8Few& f, int* stat
 }  // namespace
 
 W8a8Few w8a8_few_shape(const W8a8Args& a) {
-  W8a8Few f;
-  // a gated pair's sums for 128 tokens would leave room for one CTA on an SM
-  f.tokens = a.M <= 16 ? 16 : a.M <= 32 ? 32 : a.M <= 64 || a.w2 ? 64 : 128;
-  f.tiles = (a.d_out + kRows - 1) / kRows;
-  f.mtiles = (a.M + f.tokens - 1) / f.tokens;
-  // As many shares of d_in as still leave every CTA resident at once, two on an
-  // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
-  // One SM draws at most about 40 GB/s through TMA from HBM, so more CTAs pay up
-  // to there: 14336 -> 4096 at one token takes 49.5, 27.4, 16.8, 13.9 us with 1,
-  // 2, 4, 8 shares; tiles of fewer rows that even out the SMs' bytes won 4% at
-  // most, and lost it elsewhere.
-  const long long places = 2 * device_sm_count(), ctas = (long long)f.tiles * f.mtiles;
-  auto fits = [&](int n) { return ctas * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };
-  const int blocks = (a.d_in + kK - 1) / kK;
-  f.split = 1;
-  while (f.split < kMaxSplit && fits(2 * f.split) && 2 * f.split <= blocks) f.split *= 2;
-  return f;
+  // Token tiles with what a call costs, in ns, fitted to measured times: `base` for
+  // the set-up and the epilogue of a full tile (`alone` where no SM has two CTAs),
+  // down to the smallest tile's for an empty one, and `block` for every 128 columns
+  // of a share.  No call takes less than its weights take from HBM.  Measured with
+  // tiles of 16, 32, 64, 128 tokens, us:
+  //   1536 -> 1536:  M 128: 6.5 5.6 8.9 7.5;     M 256: 9.5 7.1 7.4 10.0
+  //   4096 -> 4096:  M 64: 11.8 9.0 10.0 10.1;   M 203: 34.6 18.7 14.5 12.5
+  //   14336 -> 4096: M 32: 17.6 14.4 15.4 15.4;  M 128: 51.3 29.2 20.4 19.0
+  //   512 -> 512:    M 100: 3.5 3.6 5.2 6.0
+  // and a gated pair with 16, 32, 64 (128 tokens' sums would leave room for one CTA
+  // on an SM):
+  //   1536 -> 1536:  M 40: 5.8 6.6 8.0;          M 203: 12.4 9.8 10.6
+  //   4096 -> 4096:  M 32: 12.4 11.4 13.0;       M 128: 26.7 18.8 16.6
+  struct Cost {
+    int tokens, base, alone, block;
+  };
+  static constexpr Cost kPlain[] = {{16, 3200, 3200, 450}, {32, 3600, 3600, 450}, {64, 7800, 5600, 450}, {128, 10200, 6800, 470}};
+  static constexpr Cost kGated[] = {{16, 4000, 4000, 620}, {32, 5200, 5200, 700}, {64, 9500, 8500, 750}};
+  const Cost* costs = a.w2 ? kGated : kPlain;
+  const int sms = device_sm_count(), blocks = (a.d_in + kK - 1) / kK;
+  const long long hbm = 4000 + (long long)a.d_in * a.d_out * (a.w2 ? 2 : 1) / 5200;
+  W8a8Few best;
+  best.ns = LLONG_MAX;
+  for (int i = 0; i < (a.w2 ? 3 : 4); ++i) {
+    const Cost& c = costs[i];
+    if (i && a.M <= costs[i - 1].tokens) break;
+    W8a8Few f;
+    f.tokens = c.tokens;
+    f.tiles = (a.d_out + kRows - 1) / kRows;
+    f.mtiles = (a.M + f.tokens - 1) / f.tokens;
+    if (f.mtiles > 65535) continue;  // grid.y
+    // As many shares of d_in as still leave every CTA resident at once, two on an
+    // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
+    // One SM draws at most about 40 GB/s through TMA from HBM, so more CTAs pay up
+    // to there: 14336 -> 4096 at one token takes 49.5, 27.4, 16.8, 13.9 us with 1,
+    // 2, 4, 8 shares; tiles of fewer rows that even out the SMs' bytes won 4% at
+    // most, and lost it elsewhere.
+    const long long places = 2 * sms, tiles = (long long)f.tiles * f.mtiles;
+    auto fits = [&](int n) { return tiles * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };
+    f.split = 1;
+    while (f.split < kMaxSplit && fits(2 * f.split) && 2 * f.split <= blocks) f.split *= 2;
+    const long long ctas = tiles * f.split, rounds = (ctas + places - 1) / places;
+    const long long rows = (long long)f.mtiles * f.tokens, full = (ctas <= sms ? c.alone : c.base) - costs[0].base;
+    f.ns = costs[0].base + full * a.M / rows + (blocks + f.split - 1) / f.split * rounds * c.block;
+    f.ns = (f.ns > hbm ? f.ns : hbm) + f.ns / 16;  // among equals of HBM, the one with less to do
+    if (f.ns < best.ns) best = f;
+  }
+  return best;
 }
 
-cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream) {
+cudaError_t launch_w8a8_few(const W8a8Args& a, const W8a8Few& f, int* status, cudaStream_t stream) {
   FewArgs A;
   if (!w8_map(&A.w, a.w, a.d_out, a.d_in, kRows) || (a.w2 && !w8_map(&A.w2, a.w2, a.d_out, a.d_in, kRows)))
     return cudaErrorInvalidValue;
@@ -389,7 +422,6 @@ cudaError_t launch_w8a8_few(const W8a8Args& a, int* status, cudaStream_t stream)
   A.M = a.M;
   A.d_out = a.d_out;
   A.blocks = (a.d_in + kK - 1) / kK;
-  const W8a8Few f = w8a8_few_shape(a);
   switch (f.tokens) {
     case 16: return launch_tn<16>(a, A, f, status, stream);
     case 32: return launch_tn<32>(a, A, f, status, stream);
