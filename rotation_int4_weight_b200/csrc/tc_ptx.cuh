@@ -48,6 +48,15 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
   return true;
 }
 
+// The same, given up (false) when *stop is set, too.
+__device__ __forceinline__ bool mbar_wait_unless(uint32_t bar, uint32_t parity, const int* stop) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_test(bar, parity))
+    if (*(const volatile int*)stop != 0 || clock64() - t0 > (1LL << 31)) return false;
+  return true;
+}
+
 // ---- clusters --------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;

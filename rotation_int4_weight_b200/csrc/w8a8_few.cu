@@ -116,44 +116,49 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     report_status(status, kStatusTimeout);
     atomicExch(&abort_flag, 1);
   };
-  auto aborted = [&]() { return *(volatile int*)&abort_flag != 0; };
+  // a wait that also ends, false, when another role gave up
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag); };
 
+  // The two loops below set the pace: each step of one thread costs 280 clocks and
+  // up (waits, barrier, copies), so stages and parities are counted, not divided,
+  // and the abort flag is looked at only while waiting.  With divisions a step took
+  // 800 clocks, which held every SM to 40 GB/s.
   if (warp == 0) {
     if (lane == 0) {
-      int i = 0;
+      int i = 0, s = 0, x = k0 * kK;
+      uint32_t phase = 1, dst = ring, bar = b_full;
 #pragma unroll 1
-      for (; i < nk; ++i) {
-        const int s = i % stages;
-        if (i >= stages && !mbar_wait(b_empty + 8 * s, ((i / stages) - 1) & 1)) { fail(); break; }
-        if (aborted()) break;
-        const uint32_t dst = ring + s * Geo::STAGE, bar = b_full + 8 * s;
-        const int x = (k0 + i) * kK;
+      for (; i < nk; ++i, x += kK) {
+        // (phase starts at 1: the first wait, a round later, is for parity 0)
+        if (i >= stages && !wait(bar + (b_empty - b_full), phase)) { fail(); break; }
         mbar_expect_tx(bar, (NW * kRows + A.xrows) * kK);
         tma_load(dst, &A.w, x, n0, bar);
         if constexpr (GATED) tma_load(dst + kRows * kK, &A.w2, x, n0, bar);
         tma_load(dst + NW * kRows * kK, &A.q, x, m0, bar);
+        if (++s == stages) s = 0, phase ^= 1, dst = ring, bar = b_full;
+        else dst += Geo::STAGE, bar += 8;
       }
       s_issued = i;
     }
   } else if (warp == 1) {
     if (lane == 0) {
       constexpr uint32_t idesc = idesc_s8(kRows, TN);
-      int i = 0;
+      int i = 0, s = 0;
+      uint32_t phase = 0, w = ring, bar = b_full;
       bool ok = true;
 #pragma unroll 1
       for (; i < nk; ++i) {
-        const int s = i % stages;
-        if (!mbar_wait(b_full + 8 * s, (i / stages) & 1)) { fail(); ok = false; break; }
-        if (aborted()) { ok = false; break; }
+        if (!wait(bar, phase)) { fail(); ok = false; break; }
         tc_fence_after();
-        const uint32_t w = ring + s * Geo::STAGE, x = w + NW * kRows * kK;
+        const uint64_t dw = desc_sw128(w), dx = desc_sw128(w + NW * kRows * kK);
 #pragma unroll
         for (int kk = 0; kk < kK / 32; ++kk)
 #pragma unroll
           for (int g = 0; g < NW; ++g)
-            mma_s8<1>(tmem + g * TN, desc_sw128(w + g * kRows * kK + kk * 32), desc_sw128(x + kk * 32), idesc,
-                      (i > 0 || kk > 0) ? 1u : 0u);
-        commit(b_empty + 8 * s);
+            mma_s8<1>(tmem + g * TN, dw + (g * kRows * kK + kk * 32) / 16, dx + kk * 2, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+        commit(bar + (b_empty - b_full));
+        if (++s == stages) s = 0, phase ^= 1, w = ring, bar = b_full;
+        else w += Geo::STAGE, bar += 8;
       }
       if (ok) commit(b_acc);
       s_committed = i;

@@ -91,26 +91,31 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     report_status(status, kStatusTimeout);
     atomicExch(&abort_flag, 1);
   };
-  auto aborted = [&]() { return *(volatile int*)&abort_flag != 0; };
+  // a wait that also ends, false, when another role gave up
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag); };
 
+  // One thread's step (wait, barrier, copies or MMAs) has to stay below the 512
+  // clocks that a stage's MMAs take: stages and parities are counted, and the abort
+  // flag is looked at only while waiting.
   if (warp == 0) {
     if (lane == 0) {
       const CUtensorMap* wmap = GATED && rank ? &A.w2 : &A.w;
-      int it = 0;
+      const uint32_t first = mapa(b_full, 0);  // the first CTA's barriers
+      int it = 0, s = 0;
+      uint32_t phase = 1;
       bool ok = true;
 #pragma unroll 1
       for (int t = pair; ok && t < A.tiles; t += pairs) {
         const int m0 = (t % A.mtiles) * kTile + rank * kHalf;
         const int n0 = (t / A.mtiles) * NC + (GATED ? 0 : rank * kHalf);
 #pragma unroll 1
-        for (int k = 0; k < A.blocks; ++k, ++it) {
-          const int s = it % kStages;
-          if (it >= kStages && !mbar_wait(b_empty + 8 * s, ((it / kStages) - 1) & 1)) { fail(); ok = false; break; }
-          if (aborted()) { ok = false; break; }
-          const uint32_t bar = mapa(b_full + 8 * s, 0), dst = ring + s * kStageBytes;
+        for (int x = 0; x < A.blocks * kK; x += kK, ++it) {
+          if (it >= kStages && !wait(b_empty + 8 * s, phase)) { fail(); ok = false; break; }
+          const uint32_t bar = first + 8 * s, dst = ring + s * kStageBytes;
           if (rank == 0) mbar_expect_tx(b_full + 8 * s, 2 * kStageBytes);
-          tma_load_pair(dst, &A.q, k * kK, m0, bar);
-          tma_load_pair(dst + kHalfBytes, wmap, k * kK, n0, bar);
+          tma_load_pair(dst, &A.q, x, m0, bar);
+          tma_load_pair(dst + kHalfBytes, wmap, x, n0, bar);
+          if (++s == kStages) s = 0, phase ^= 1;
         }
       }
       s_issued = it;
@@ -118,27 +123,25 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
       constexpr uint32_t idesc = idesc_s8(kTile, kTile);
-      int it = 0, j = 0;
+      int it = 0, j = 0, s = 0;
+      uint32_t phase = 0;
       bool ok = true;
 #pragma unroll 1
       for (int t = pair; ok && t < A.tiles; t += pairs, ++j) {
-        const int acc = j & 1;
-        if (j >= 2 && !mbar_wait(b_acc_empty + 8 * acc, ((j >> 1) - 1) & 1)) { fail(); break; }
+        const uint32_t acc = tmem + (j & 1) * kTile;
+        if (j >= 2 && !wait(b_acc_empty + 8 * (j & 1), ((j >> 1) - 1) & 1)) { fail(); break; }
         tc_fence_after();
 #pragma unroll 1
         for (int k = 0; k < A.blocks; ++k, ++it) {
-          const int s = it % kStages;
-          if (!mbar_wait(b_full + 8 * s, (it / kStages) & 1)) { fail(); ok = false; break; }
-          if (aborted()) { ok = false; break; }
+          if (!wait(b_full + 8 * s, phase)) { fail(); ok = false; break; }
           tc_fence_after();
-          const uint32_t a = ring + s * kStageBytes, b = a + kHalfBytes;
+          const uint64_t a = desc_sw128(ring + s * kStageBytes), b = desc_sw128(ring + s * kStageBytes + kHalfBytes);
 #pragma unroll
-          for (int kk = 0; kk < kK / 32; ++kk)
-            mma_s8<2>(tmem + acc * kTile, desc_sw128(a + kk * 32), desc_sw128(b + kk * 32), idesc,
-                      (k > 0 || kk > 0) ? 1u : 0u);
+          for (int kk = 0; kk < kK / 32; ++kk) mma_s8<2>(acc, a + kk * 2, b + kk * 2, idesc, (k > 0 || kk > 0) ? 1u : 0u);
           commit_pair(b_empty + 8 * s);
+          if (++s == kStages) s = 0, phase ^= 1;
         }
-        if (ok) commit_pair(b_acc_full + 8 * acc);
+        if (ok) commit_pair(b_acc_full + 8 * (j & 1));
       }
       s_committed = it;
     }
@@ -162,7 +165,7 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         if constexpr (!GATED) s_bias[acc][c] = A.bias && n < A.d_out ? from_16<F16>(A.bias[n]) : 0.0f;
       }
       asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kEpiWarps) : "memory");
-      if (!mbar_wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
+      if (!wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = half * (NC / 2); c0 < (half + 1) * (NC / 2) && n0 + c0 < A.d_out; c0 += 32) {
