@@ -139,6 +139,28 @@ __device__ __forceinline__ void store_part(T* p, const Chunk<T>& c, int lo, int 
     if (e >= lo && e < hi) reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(c.w[e / 2] >> (16 * (e & 1)));
 }
 
+// The chunk at p, columns c .. c + kW - 1 of a row of d, cut to the row: STEP as
+// the kernel's.
+template <typename T, int STEP>
+__device__ __forceinline__ Chunk<T> load_chunk(const T* p, int c, int d) {
+  if constexpr (STEP == 16) return load_vec(p);
+  if (c >= 0 && c + kW <= d) return load_vec(p);
+  if constexpr (STEP == 1) return load_part(p, -c, d - c);
+  Chunk<T> o = {};
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(o) / 32); ++i) {
+    const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+    o.w[4 * i] = u.x, o.w[4 * i + 1] = u.y, o.w[4 * i + 2] = u.z, o.w[4 * i + 3] = u.w;
+  }
+  return o;
+}
+template <typename T, int STEP>
+__device__ __forceinline__ void store_chunk(T* p, const Chunk<T>& v, int c, int d) {
+  if (STEP == 16 || (c >= 0 && c + kW <= d)) store_vec(p, v);
+  else if (STEP == 1) store_part(p, v, -c, d - c);
+  else *reinterpret_cast<uint4*>(p) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+}
+
 // gain[c .. c + kW - 1], columns outside 0 .. d - 1 zero.  c & 7 is the same for
 // all chunks of a row.
 template <typename T>
@@ -238,11 +260,13 @@ __device__ __forceinline__ bool out_of_range(float ss) { return !(ss <= 3.0e38f)
 
 // threadIdx.x runs over a row's chunks (NC of them a thread, blockDim.x apart),
 // threadIdx.y over the rows of the CTA (more than one only at 32 threads a row).
-// EVEN: d is a multiple of kW, every chunk is whole and starts at a column
-// multiple of kW.
-template <typename T, int NC, bool NORM, bool EVEN>
+// STEP: 16 or 8 where d is a multiple of it, every chunk starts at a column
+// multiple of kW, and with 8 the last may be half and codes are stored by 8 bytes;
+// else 1.
+template <typename T, int NC, bool NORM, int STEP>
 __global__ void __launch_bounds__(1024)
 codes_kernel(const CodeArgs A) {
+  constexpr bool EVEN = STEP > 1;
   __shared__ uint32_t red_a[32];
   __shared__ float red_s[32];
   ptx::grid_trigger();
@@ -271,10 +295,9 @@ codes_kernel(const CodeArgs A) {
     for (int i = 0; i < NC; ++i) {
       const int j = threadIdx.x + i * T1, c = j * kW - head;
       if (j < chunks) {
-        const bool whole = EVEN || (c >= 0 && c + kW <= d);
-        h[i] = whole ? load_vec(x + j * kW) : load_part(x + j * kW, -c, d - c);
+        h[i] = load_chunk<T, STEP>(x + j * kW, c, d);
         if constexpr (NORM)
-          if (with_res) r[i] = whole ? load_vec(res + j * kW) : load_part(res + j * kW, -c, d - c);
+          if (with_res) r[i] = load_chunk<T, STEP>(res + j * kW, c, d);
       }
     }
     if constexpr (NORM)
@@ -284,8 +307,7 @@ codes_kernel(const CodeArgs A) {
           const int j = threadIdx.x + i * T1, c = j * kW - head;
           if (j < chunks) {
             add_to(h[i], r[i]);
-            if (EVEN || (c >= 0 && c + kW <= d)) store_vec(hid + j * kW, h[i]);
-            else store_part(hid + j * kW, h[i], -c, d - c);
+            store_chunk<T, STEP>(hid + j * kW, h[i], c, d);
           }
         }
       }
@@ -294,7 +316,7 @@ codes_kernel(const CodeArgs A) {
   auto row_values = [&](int i, int j, float (&v)[kW]) {
     values(h[i], v);
     if constexpr (NORM)
-      if (with_gain) times(v, EVEN ? load_vec(gain + j * kW) : load_gain(gain, j * kW - head, d));
+      if (with_gain) times(v, EVEN ? load_chunk<T, STEP>(gain + j * kW, j * kW, d) : load_gain(gain, j * kW - head, d));
   };
   uint32_t wide = 0u;  // bits of the largest |v|
   float ss = 0.0f;
@@ -307,7 +329,7 @@ codes_kernel(const CodeArgs A) {
         values(h[i], v);
 #pragma unroll
         for (int e = 0; e < kW; ++e) ss = fmaf(v[e], v[e], ss);
-        if (with_gain) times(v, EVEN ? load_vec(gain + j * kW) : load_gain(gain, j * kW - head, d));
+        if (with_gain) times(v, EVEN ? load_chunk<T, STEP>(gain + j * kW, j * kW, d) : load_gain(gain, j * kW - head, d));
         Chunk<float> c;
 #pragma unroll
         for (int e = 0; e < kW; ++e) c.w[e] = __float_as_uint(v[e]);
@@ -376,7 +398,10 @@ codes_kernel(const CodeArgs A) {
         for (int e = 0; e < kW; ++e) v[e] = finite ? v[e] * up : 0.0f;
       }
       const uint4 o = codes_of(v, a, inv);
-      if (EVEN || (c >= 0 && c + kW <= d)) {
+      if (STEP == 8) {
+        *reinterpret_cast<uint2*>(q + j * kW) = make_uint2(o.x, o.y);
+        if (c + kW <= d) *reinterpret_cast<uint2*>(q + j * kW + 8) = make_uint2(o.z, o.w);
+      } else if (EVEN || (c >= 0 && c + kW <= d)) {
         *reinterpret_cast<uint4*>(q + j * kW) = o;
       } else {
         const uint32_t w[4] = {o.x, o.y, o.z, o.w};
@@ -389,7 +414,7 @@ codes_kernel(const CodeArgs A) {
   if (threadIdx.x == 0) A.sx[row] = row_scale<NORM>(amax, finite, ss, hs, d, A.eps);
 }
 
-template <typename T, bool NORM, bool EVEN>
+template <typename T, bool NORM, int STEP>
 cudaError_t launch_nc(const CodeArgs& A, int nc, int threads, cudaStream_t s) {
   const int rows = threads == 32 ? 4 : 1;
   cudaLaunchConfig_t cfg = {};
@@ -401,9 +426,9 @@ cudaError_t launch_nc(const CodeArgs& A, int nc, int threads, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (nc <= 1) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 1, NORM, EVEN>, A);
-  if (nc <= 2) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 2, NORM, EVEN>, A);
-  return cudaLaunchKernelEx(&cfg, codes_kernel<T, 4, NORM, EVEN>, A);
+  if (nc <= 1) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 1, NORM, STEP>, A);
+  if (nc <= 2) return cudaLaunchKernelEx(&cfg, codes_kernel<T, 2, NORM, STEP>, A);
+  return cudaLaunchKernelEx(&cfg, codes_kernel<T, 4, NORM, STEP>, A);
 }
 
 template <typename T, bool NORM>
@@ -415,14 +440,16 @@ cudaError_t launch_rows(const CodeArgs& A, cudaStream_t s) {
   // 1, 2, 4 chunks (bf16): norm 2048 x 4096: 15.6, 13.7, 18.1; 4096 x 8192: 54.7,
   // 43.7, 54.0; codes 2048 x 1536: 4.7, 6.9, 8.5; 4096 x 8192: 25.2, 23.9, 23.2;
   // 2048 x 14336: 32.8, 23.9, 21.5; fp32 14336 x 4096: 45.0, 44.4, 62.1.
-  const int chunks = A.d % kW ? A.d / kW + 2 : A.d / kW;
+  const int chunks = A.d % 8 ? A.d / kW + 2 : (A.d + kW - 1) / kW;
   const bool few = A.M * chunks <= (long long)device_sm_count() * 1024;
   const int want = few ? 1 : NORM || sizeof(T) == 4 ? 2 : chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4;
   int threads = ((chunks + want - 1) / want + 31) / 32 * 32;
   if (threads > 1024) threads = 1024;
   const int need = (chunks + threads - 1) / threads;
   if (need > 4) return cudaErrorInvalidValue;
-  return A.d % kW == 0 ? launch_nc<T, NORM, true>(A, need, threads, s) : launch_nc<T, NORM, false>(A, need, threads, s);
+  if (A.d % 16 == 0) return launch_nc<T, NORM, 16>(A, need, threads, s);
+  if constexpr (sizeof(T) == 4) return cudaErrorInvalidValue;  // weights' rows are whole chunks
+  else return A.d % 8 == 0 ? launch_nc<T, NORM, 8>(A, need, threads, s) : launch_nc<T, NORM, 1>(A, need, threads, s);
 }
 
 }  // namespace

@@ -64,21 +64,21 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
 }
 
 // The kernel with the smaller estimate, both fits to measured times (bf16, GPU time
-// of calls in a row, weights from HBM).  The kernel for many tokens takes 0.375 us
-// per 128 columns and round of tiles (256 x 256 on a pair of SMs) and 6 us around
-// it, 6 more where rows of y are not whole 16 bytes, which no TMA store can write.
+// of calls in a row, weights from HBM).  The kernel for many tokens takes 0.35 us
+// per 128 columns and round of tiles (256 x 256 on a pair of SMs) and 5.6 us around
+// it, 4 more where rows of y are not whole 16 bytes, which no TMA store can write.
 // Measured, few / many, us:
-//   4096 -> 4096:  M 256: 12.6 / 17.9, M 512: 17.5 / 18.0, M 768: 26.0 / 18.5;
-//   4096 -> 14336: M 128: 20.6 / 19.4, M 129: 27.2 / 19.5, M 512: 53.4 / 31.7;
-//   1552 -> 1100:  M 203: 6.8 / 16.3, M 1536: 14.4 / 17.2;
-//   gated 1536 -> 8960: M 33: 12.4 / 14.5, M 129: 21.3 / 12.3;
-//   gated 14336 -> 4096: M 128: 35.1 / 48.5, M 129: 52.5 / 48.5.
+//   4096 -> 4096:  M 256: 12.9 / 17, M 512: 17.0 / 17, M 768: 26 / 17.5;
+//   4096 -> 14336: M 100: 19.2 / 18.5, M 129: 27 / 18.5, M 512: 53 / 29.6;
+//   1552 -> 1100:  M 203: 6.5 / 12;
+//   gated 1536 -> 8960: M 33: 11 / 14, M 129: 21 / 11.9;
+//   gated 14336 -> 4096: M 128: 33.8 / 45, M 129: 52 / 45.
 cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream) {
   const W8a8Few f = w8a8_few_shape(a);
   const long long blocks = (a.d_in + 127) / 128, pairs = device_sm_count() / 2;
   const int nc = a.w2 ? 128 : 256;
   const long long tiles = ((a.M + 255LL) / 256) * ((a.d_out + nc - 1) / nc);
-  const long long many = 6000 + (a.d_out % 8 ? 6000 : 0) + (tiles + pairs - 1) / pairs * blocks * 375;
+  const long long many = 5600 + (a.d_out % 8 ? 4000 : 0) + (tiles + pairs - 1) / pairs * blocks * 350;
   return a.M <= 32 || f.ns <= many ? launch_w8a8_few(a, f, status, stream) : launch_w8a8_many(a, status, stream);
 }
 

@@ -315,9 +315,22 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   }
 }
 
+// tcgen05.alloc waits for columns to come free, and a CTA waits for its cluster's:
+// two launches at once must never wait for each other.  They cannot, because the
+// CTAs that an SM's shared memory lets in never want more than its 512 columns,
+// and one that takes all 512 (w8a8_many, w4_tc) leaves no shared memory for another.
+template <int TN, bool GATED>
+constexpr int least_smem() {
+  using Geo = FewGeo<TN, GATED>;
+  return 1024 + (Geo::STORED ? Geo::STAGE + Geo::SUMS : Geo::STAGE > Geo::SUMS ? Geo::STAGE : Geo::SUMS);
+}
+
 template <int TN, bool GATED, bool F16>
 cudaError_t launch_few(FewArgs& A, const W8a8Few& f, int* status, cudaStream_t stream) {
   using Geo = FewGeo<TN, GATED>;
+  constexpr int kSmSmem = 228 * 1024;
+  static_assert(kSmSmem / least_smem<TN, GATED>() * Geo::COLS <= 512, "tensor memory of the CTAs that fit an SM");
+  static_assert(least_smem<TN, GATED>() > 16 * 1024, "no room beside a CTA with all of tensor memory");
   const int per = (A.blocks + f.split - 1) / f.split;
   A.split = f.split;
   constexpr int kBudget = 104 * 1024;  // of 228 KB, for two CTAs
@@ -381,7 +394,7 @@ W8a8Few w8a8_few_shape(const W8a8Args& a) {
   struct Cost {
     int tokens, base, alone, block;
   };
-  static constexpr Cost kPlain[] = {{16, 3200, 3200, 450}, {32, 3600, 3600, 450}, {64, 7800, 5600, 450}, {128, 10200, 6800, 470}};
+  static constexpr Cost kPlain[] = {{16, 3200, 3200, 450}, {32, 3600, 3600, 450}, {64, 7800, 5600, 450}, {128, 9500, 6800, 470}};
   static constexpr Cost kGated[] = {{16, 4000, 4000, 620}, {32, 5200, 5200, 700}, {64, 9500, 8500, 750}};
   const Cost* costs = a.w2 ? kGated : kPlain;
   const int sms = device_sm_count(), blocks = (a.d_in + kK - 1) / kK;

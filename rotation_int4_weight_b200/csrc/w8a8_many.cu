@@ -25,11 +25,15 @@ namespace {
 
 using namespace ptx;
 
-constexpr int kTile = 256, kHalf = 128, kK = 128, kStages = 6;
+constexpr int kTile = 256, kHalf = 128, kK = 128, kStages = 5;
 constexpr int kEpiWarps = 8, kThreads = 64 + 32 * kEpiWarps;
-constexpr int kOutBytes = 32 * 64;  // a warp's 32 tokens x 32 channels on their way out
+constexpr int kOutBytes = 32 * 64;  // a warp's 32 tokens x 32 channels on their way out; two of them a warp
 constexpr int kHalfBytes = kHalf * kK, kStageBytes = 2 * kHalfBytes;
-constexpr int kSmem = kStages * kStageBytes + kEpiWarps * kOutBytes + 1024;
+constexpr int kUsed = kStages * kStageBytes + 2 * kEpiWarps * kOutBytes + 1024;
+// The CTA takes all of tensor memory, so it asks for more shared memory than it
+// uses: none that wants tensor memory beside it may fit the same SM (w8a8_few.cu).
+constexpr int kSmem = 216 * 1024;
+static_assert(kUsed <= kSmem && kSmem >= (228 - 16) * 1024, "shared memory of a CTA");
 
 struct ManyArgs {
   CUtensorMap q, w, w2, out;  // out: y in boxes of 32 x 32, where its rows are a multiple of 16 bytes
@@ -147,10 +151,10 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
-    unsigned char* out = smem + kStages * kStageBytes + (warp - 2) * kOutBytes;
+    unsigned char* out = smem + kStages * kStageBytes + (warp - 2) * 2 * kOutBytes;
     const bool by_tma = (A.d_out & 7) == 0;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
-    int j = 0;
+    int j = 0, turn = 0;
 #pragma unroll 1
     for (int t = pair; t < A.tiles; t += pairs, ++j) {
       const int acc = j & 1;
@@ -194,26 +198,35 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
           o[c / 2 + 1] = to_16<F16>(f[2]) | ((uint32_t)to_16<F16>(f[3]) << 16);
         }
         // row = token, 64 bytes, its 16-byte parts swapped by bits 1-2 of the row
-        bulk_read_wait();  // the last box has left this warp's part
+        unsigned char* box = out + turn * kOutBytes;
+        turn ^= 1;
+        bulk_read_wait<1>();  // the box before the last has left its place
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(out + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+          *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
         const int m_warp = m - lane;
         if (by_tma) {
           async_fence();
           __syncwarp();
           if (lane == 0 && m_warp < A.M) {
-            tma_store(&A.out, smem_u32(out), n, m_warp);
+            tma_store(&A.out, smem_u32(box), n, m_warp);
             bulk_commit();
           }
         } else {
+          // rows of y at any even address: 32 or, where rows start on 4 bytes, 2 x 16 lanes side by side
           __syncwarp();
-          for (int r = 0; r < 32 && m_warp + r < A.M; ++r)
-            if (n + lane < A.d_out)
-              A.y[(size_t)(m_warp + r) * A.d_out + n + lane] = *reinterpret_cast<const uint16_t*>(
-                  out + r * 64 + (((lane >> 3) ^ ((r >> 1) & 3)) << 4) + (lane & 7) * 2);
+          const int wide = (A.d_out & 1) == 0, c = wide ? 2 * (lane & 15) : lane;
+#pragma unroll 8
+          for (int r = wide ? lane >> 4 : 0; r < 32; r += 1 + wide) {
+            const unsigned char* from = box + r * 64 + (((c >> 3) ^ ((r >> 1) & 3)) << 4) + (c & 7) * 2;
+            uint16_t* to = A.y + (size_t)(m_warp + r) * A.d_out + n + c;
+            if (m_warp + r < A.M && n + c < A.d_out) {
+              if (wide) *reinterpret_cast<uint32_t*>(to) = *reinterpret_cast<const uint32_t*>(from);
+              else *to = *reinterpret_cast<const uint16_t*>(from);
+            }
+          }
         }
       }
       __syncwarp();

@@ -411,6 +411,26 @@ def test_two_streams_at_once():
     _status_ok()
 
 
+def test_both_linear_kernels_at_once():
+    # pairs of CTAs with all of tensor memory and clusters with some of it, on three
+    # streams: neither may take what the other's half waits for
+    big, small = _operands(1500, 2064, 2048, 1)[:4], _operands(100, 2064, 2048, 2)[:4]
+    gate = _operands(40, 512, 1552, 3)[:6]
+    calls = [lambda s: paro.paro_w8a8_linear(*big, stream=s), lambda s: paro.paro_w8a8_linear(*small, stream=s),
+             lambda s: paro.paro_w8a8_swiglu(*gate, stream=s)]
+    alone = [c(None) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[] for _ in calls]
+    for _ in range(40):
+        for k, c in enumerate(calls):
+            got[k].append(c(streams[k]))
+    torch.cuda.synchronize()
+    for k, ys in enumerate(got):
+        assert all(torch.equal(y, alone[k]) for y in ys)
+    _status_ok()
+
+
 def test_codes_of_a_matrix_as_weights_right_away():
     # the row codes of a 16-bit matrix are weights too: the linear right behind the call
     # that wrote them reads them whole
@@ -447,6 +467,28 @@ def test_rotate_w8a8_linear(M, d_in, d_out):
     full = x.double() @ W.double().T + bias.double()
     slack = 2.0 ** -7 * (full.abs() + (xt.abs() @ wt.abs().T))
     assert ((y.double() - full).abs() <= near + slack).all()
+
+
+def test_rotate_w8a8_linear_without_a_transform():
+    # K = 0 and no scale: the plain 8-bit linear on bf16 activations
+    x = _acts(5, 512, BF16, 1, spread=False)
+    qw, sw = paro.paro_pack_weights_int8(torch.randn(96, 512, device=DEV))
+    y = paro.paro_rotate_w8a8_linear(x, None, None, None, None, qw, sw)
+    _status_ok()
+    q, sx = paro.paro_quantize_activations_int8(x)
+    assert torch.equal(y, paro.paro_w8a8_linear(q, sx, qw, sw))
+
+
+@pytest.mark.parametrize("d", [8, 24, 4088, 8184, 49144])
+@pytest.mark.parametrize("M", [3, 700])
+def test_norm_of_widths_that_are_multiples_of_8_only(M, d):
+    x, r = _acts(M, d, BF16, 1), _acts(M, d, BF16, 2)
+    gain = _acts(1, d, BF16, 3, spread=False)[0]
+    q, sx, h = paro.paro_rms_norm_int8(x, gain, r)
+    assert torch.equal(h, (x.double() + r.double()).to(BF16))
+    rq, rs = oracle.rms_norm_codes(_f64(h), _f64(gain), float(np.float32(1e-6)))
+    assert np.array_equal(q.cpu().numpy(), rq)
+    _scales_close(sx, rs, 40)
 
 
 def test_refusals():
