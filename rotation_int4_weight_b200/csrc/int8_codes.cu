@@ -123,13 +123,12 @@ __device__ __forceinline__ void store_vec(T* p, const Chunk<T>& c) {
 // Values lo .. hi - 1 of the chunk at p (the others zero), one by one.
 __device__ __forceinline__ uint32_t bits(const __nv_bfloat16* p) { return *reinterpret_cast<const uint16_t*>(p); }
 __device__ __forceinline__ uint32_t bits(const __half* p) { return *reinterpret_cast<const uint16_t*>(p); }
-__device__ __forceinline__ uint32_t bits(const float* p) { return __float_as_uint(*p); }
 template <typename T>
 __device__ __forceinline__ Chunk<T> load_part(const T* p, int lo, int hi) {
   Chunk<T> c = {};
 #pragma unroll
   for (int e = 0; e < kW; ++e)
-    if (e >= lo && e < hi) c.w[e * sizeof(T) / 4] |= bits(p + e) << (sizeof(T) == 2 ? 16 * (e & 1) : 0);
+    if (e >= lo && e < hi) c.w[e / 2] |= bits(p + e) << (16 * (e & 1));
   return c;
 }
 template <typename T>
@@ -433,16 +432,16 @@ cudaError_t launch_nc(const CodeArgs& A, int nc, int threads, cudaStream_t s) {
 
 template <typename T, bool NORM>
 cudaError_t launch_rows(const CodeArgs& A, cudaStream_t s) {
-  // Chunks a thread takes.  One while all rows' threads fit the GPU at once, where
-  // a row's latency counts.  Else each row costs its threads the same instructions
-  // for addresses, reduction and scale, so fewer threads with more chunks gain,
-  // until too few rows are in flight or registers run out.  Measured, us, with
-  // 1, 2, 4 chunks (bf16): norm 2048 x 4096: 15.6, 13.7, 18.1; 4096 x 8192: 54.7,
-  // 43.7, 54.0; codes 2048 x 1536: 4.7, 6.9, 8.5; 4096 x 8192: 25.2, 23.9, 23.2;
-  // 2048 x 14336: 32.8, 23.9, 21.5; fp32 14336 x 4096: 45.0, 44.4, 62.1.
+  // Chunks a thread takes.  Each row costs its threads the same instructions for
+  // addresses, reduction and scale, so fewer threads with more chunks gain, as long
+  // as enough of them are in flight and registers last (a norm's do for two chunks).
+  // Measured, us, with 1, 2, 4 chunks (bf16): norm 300 x 8960: 8.0, 7.0, 10.6; 2048
+  // x 4096: 15.6, 13.7, 18.1; 4096 x 8192: 54.7, 43.7, 54.0; codes 300 x 8960: 4.7,
+  // 6.1, 8.8; 2048 x 1536: 4.7, 6.9, 8.5; 4096 x 8192: 25.2, 23.9, 23.2; 2048 x
+  // 14336: 32.8, 23.9, 21.5; fp32 14336 x 4096: 45.0, 44.4, 62.1.
   const int chunks = A.d % 8 ? A.d / kW + 2 : (A.d + kW - 1) / kW;
-  const bool few = A.M * chunks <= (long long)device_sm_count() * 1024;
-  const int want = few ? 1 : NORM || sizeof(T) == 4 ? 2 : chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4;
+  const long long per_sm = A.M * chunks / device_sm_count();
+  const int want = NORM ? (per_sm >= 1024 ? 2 : 1) : sizeof(T) == 2 && per_sm >= 8192 ? 4 : per_sm >= 2048 ? 2 : 1;
   int threads = ((chunks + want - 1) / want + 31) / 32 * 32;
   if (threads > 1024) threads = 1024;
   const int need = (chunks + threads - 1) / threads;
