@@ -491,6 +491,26 @@ def test_norm_of_widths_that_are_multiples_of_8_only(M, d):
     _scales_close(sx, rs, 40)
 
 
+def test_offsets_beyond_32_bits():
+    # more than 2^31 values in x, q and y: the first and last rows are looked at
+    M, d = 70001, 32768
+    x = torch.zeros(M, d, dtype=BF16, device=DEV)
+    rows = [0, 65535, 65536, M - 1]
+    x[rows] = _acts(4, d, BF16, 1)
+    q, sx = paro.paro_quantize_activations_int8(x)
+    rq, rs = oracle.row_codes(_f64(x[rows]))
+    assert np.array_equal(q[rows].cpu().numpy(), rq)
+    _scales_close(sx[rows], rs, 1)
+    assert not q[1000].any() and not q[65537:].any(1)[:-1].any()
+    del x, q
+    M, d_in, d_out = 70001, 32, 32000
+    q, sx, w, sw, _, _, _ = _operands(M, d_in, d_out, 2)
+    y = paro.paro_w8a8_linear(q, sx, w, sw)
+    _status_ok()
+    rows = [0, 1, 67107, 67108, 67109, M - 2, M - 1]   # 2^31 / 32000 = 67108.9
+    assert_linear(y[rows], q[rows], sx[rows], w, sw)
+
+
 def test_refusals():
     q = torch.zeros(2, 64, dtype=torch.int8, device=DEV)
     s, w, sw = torch.ones(2, device=DEV), torch.zeros(8, 64, dtype=torch.int8, device=DEV), torch.ones(8, device=DEV)

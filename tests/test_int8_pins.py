@@ -127,7 +127,7 @@ LINEAR = dict(q=X, sx=S, w=W, ws=WS, b=None, y=Y, M=4, d_in=512, d_out=100, t=0)
     (dict(q=None), INVALID), (dict(q=MIS), INVALID), (dict(w=None), INVALID), (dict(w=P(256, 4)), INVALID),
     (dict(ws=P(320, 2)), INVALID), (dict(sx=None), INVALID), (dict(y=P(384, 2)), INVALID), (dict(b=P(512, 1)), INVALID),
     (dict(y=X), INVALID), (dict(y=S), INVALID), (dict(y=P(256, 64)), INVALID), (dict(y=WS), INVALID),
-    (dict(b=P(384, 2)), INVALID),
+    (dict(b=P(384, 2)), INVALID), (dict(M=(1 << 30) + 1, d_in=16), UNSUPPORTED), (dict(d_out=(1 << 30) + 1, d_in=16), UNSUPPORTED),
 ])
 def test_w8a8_linear_validation(change, expect):
     a = LINEAR | change
