@@ -22,7 +22,7 @@
 // multiples of 16 of the flat index, not of the column, so that rows of an odd
 // width still move as 16-byte loads and stores; the first and last chunk of such
 // a row go value by value, and its gain comes from aligned 16-byte loads shifted
-// by the row's phase.  For many rows the instructions, about 10 a value, and HBM
+// by the row's phase.  For many rows the instructions, about 14 a value, and HBM
 // bound it alike: 2048 x 4096 bf16 with a residual in 13.7 us (4.3 TB/s), 4096 x
 // 8192 in 43.7 us (5.4 TB/s), packing 14336 x 4096 fp32 in 44.4 us (6.6 TB/s);
 // for one row its latency does (2.5 us).

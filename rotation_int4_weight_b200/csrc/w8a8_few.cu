@@ -20,6 +20,11 @@
 // Whole sums: the order of the shares does not matter, there is no workspace and
 // nothing to reset between calls.
 //
+// Bound by the weights from HBM and about 3 us of set-up, first loads and shares'
+// sums around them: one token 4096 -> 14336 in 13.5 us (58.7 MB, 4.4 TB/s), 14336 ->
+// 4096 in 13.3 us, gated 4096 -> 14336 in 22.7 us (5.2 TB/s), 1536 -> 1536 in 3.5 us;
+// between 4096 -> 4096 and 14336 -> 4096 the added bytes come at 6.0 TB/s.
+//
 // The launch overlaps the kernel before it: until that one is done a CTA sets up
 // its barriers and asks for its weights in L2 only, which is right whoever wrote
 // them last; every read and write of its own comes after the wait.
@@ -411,9 +416,10 @@ W8a8Few w8a8_few_shape(const W8a8Args& a) {
     if (f.mtiles > 65535) continue;  // grid.y
     // As many shares of d_in as still leave every CTA resident at once, two on an
     // SM: clusters of 4 and 8 do not fill every GPC (284 and 264 of 296 places).
-    // One SM draws at most about 40 GB/s through TMA from HBM, so more CTAs pay up
-    // to there: 14336 -> 4096 at one token takes 49.5, 27.4, 16.8, 13.9 us with 1,
-    // 2, 4, 8 shares; tiles of fewer rows that even out the SMs' bytes won 4% at
+    // One CTA draws at most about 60 GB/s from HBM, so more of them pay up to there:
+    // with 1, 2, 4, 8 shares 14336 -> 4096 at one token takes 34.1, 19.6, 13.9, 13.3
+    // us, 4096 -> 14336 14.3, 13.6, 15.6, 20.5, gated 1536 -> 8960 at 16 tokens 13.5,
+    // 9.5, 9.1, 15.8.  Tiles of fewer rows that even out the SMs' bytes won 4% at
     // most, and lost it elsewhere.
     const long long places = 2 * sms, tiles = (long long)f.tiles * f.mtiles;
     auto fits = [&](int n) { return tiles * n <= (n == 8 ? places * 8 / 9 : n == 4 ? places * 19 / 20 : places); };

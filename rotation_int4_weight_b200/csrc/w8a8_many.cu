@@ -13,6 +13,11 @@
 //             time; scales, gate or bias, rounding, then through shared memory
 //             (64-byte swizzle) and a TMA store, which writes whole sectors and
 //             leaves out what lies outside y.
+// A 256 x 256 tile on a pair reads each operand once for both SMs' tensor cores, 32
+// KB an SM for 512 clocks of MMAs; a 128 x 256 tile on one SM would read 48.
+// Bound by the tensor cores under the power cap, and by the last round of tiles:
+// 2048 tokens 14336 -> 4096 in 84.5 us (2.85 PFLOP/s; 99 us when it runs for
+// seconds), gated 4096 -> 14336 in 164 us (2.93).
 // Two sets of sums (2 x 256 columns of tensor memory) let the next tile's MMAs
 // run under a tile's epilogue.  Every wait is bounded.
 #include "int8.cuh"
