@@ -20,7 +20,7 @@ namespace {
 // Interned names and what the module keeps of torch.
 PyObject *n_dtype, *n_shape, *n_device, *n_get_device, *n_is_contiguous, *n_data_ptr;
 PyObject *t_int8, *t_f32, *t_bf16, *t_f16, *t_int16, *t_uint16, *t_uint8;
-PyObject *f_empty, *f_stream, *f_device, *k_empty, *f_check;
+PyObject *f_empty, *f_empty_like, *f_stream, *f_device, *k_empty, *f_check;
 
 // The C ABI's entry points, as the library that __init__.py loaded has them.
 struct Api {
@@ -134,6 +134,18 @@ bool stream_of(int dev, paro_stream_t* out) {
   return !PyErr_Occurred();
 }
 
+// A new tensor (or null after an error) with its address in *out.
+PyObject* addressed(PyObject* made, void** out) {
+  if (!made) return nullptr;
+  Ref p(method(made, n_data_ptr));
+  if (!p.p) {
+    Py_DECREF(made);
+    return nullptr;
+  }
+  *out = PyLong_AsVoidPtr(p.p);
+  return made;
+}
+
 // `t` itself after its check, or a new tensor beside `like`; its address to *out.
 PyObject* output(PyObject* t, PyObject* dtype, int n, const long long* sizes, int dev, PyObject* like, const char* name,
                  void** out) {
@@ -150,15 +162,7 @@ PyObject* output(PyObject* t, PyObject* dtype, int n, const long long* sizes, in
   if (n > 1) args[k++] = b.p;
   args[k] = dtype;
   args[k + 1] = d.p;
-  PyObject* made = PyObject_Vectorcall(f_empty, args, k, k_empty);
-  if (!made) return nullptr;
-  Ref p(method(made, n_data_ptr));
-  if (!p.p) {
-    Py_DECREF(made);
-    return nullptr;
-  }
-  *out = PyLong_AsVoidPtr(p.p);
-  return made;
+  return addressed(PyObject_Vectorcall(f_empty, args, k, k_empty), out);
 }
 
 // Raises ParoError for a status that is not OK.
@@ -218,7 +222,9 @@ PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (!t.p || !act_type(t.p, &ty) || !address(v[0], t.p, 2, d, dev, "x", &x) ||
       !address(v[2], t.p, 2, d, dev, "residual", &r) || !address(v[1], t.p, 1, d + 1, dev, "gain", &g))
     return nullptr;
-  Ref oh(given(v[2]) ? output(v[4], t.p, 2, d, dev, v[0], "hidden", &h) : Py_NewRef(Py_None));
+  Ref oh(!given(v[2])  ? Py_NewRef(Py_None)
+         : given(v[4]) ? output(v[4], t.p, 2, d, dev, v[0], "hidden", &h)
+                       : addressed(PyObject_CallOneArg(f_empty_like, v[0]), &h));
   if (!oh.p) return nullptr;
   Ref oq(output(v[5], t_int8, 2, d, dev, v[0], "q", &q));
   if (!oq.p) return nullptr;
@@ -360,7 +366,8 @@ PyObject* setup(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (!c.p || !get(v[0], "int8", &t_int8) || !get(v[0], "float32", &t_f32) || !get(v[0], "bfloat16", &t_bf16) ||
       !get(v[0], "float16", &t_f16) || !get(v[0], "int16", &t_int16) || !get(v[0], "uint16", &t_uint16) ||
       !get(v[0], "uint8", &t_uint8) ||
-      !get(v[0], "empty", &f_empty) || !get(c.p, "_cuda_getCurrentRawStream", &f_stream) ||
+      !get(v[0], "empty", &f_empty) ||
+      !get(v[0], "empty_like", &f_empty_like) || !get(c.p, "_cuda_getCurrentRawStream", &f_stream) ||
       !get(c.p, "_cuda_getDevice", &f_device))
     return nullptr;
   f_check = Py_NewRef(v[1]);
