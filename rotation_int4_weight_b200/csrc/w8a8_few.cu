@@ -43,7 +43,11 @@ using namespace ptx;
 constexpr int kRows = 128, kK = 128, kThreads = 192;
 constexpr int kMaxSmem = 105 * 1024;  // a CTA's ring, or its sums
 constexpr int kMaxStages = 8, kMaxSplit = 8;  // 8: the portable size of a cluster
-constexpr int kAhead = 4;  // stages asked for in L2 before the kernel before is done
+// Stages asked for in L2 before the kernel before is done.  With 0, 2, 4, 16: one
+// token 4096 -> 4096 7.3, 6.6, 6.6, 6.6 us, 14336 -> 4096 13.7, 13.7, 13.3, 13.8,
+// gated 16 tokens 1536 -> 8960 9.4, 8.7, 9.1, 9.1, 203 tokens 1552 -> 1100 6.0, 6.2,
+// 6.5, 6.5, gated 4096 -> 14336 23.9, 23.3, 23.5, 28.0.
+constexpr int kAhead = 2;
 
 struct FewArgs {
   CUtensorMap w, w2, q;
