@@ -252,7 +252,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
       // [share][its slot of the owner's tokens][NW][128]
       const uint32_t sums = ring + stages * Geo::STAGE;
       const int shift = 31 - __clz(split), slots = (tokens + split - 1) >> shift;  // split: a power of two
-      const bool good = mbar_wait(b_acc, 0);
+      const bool good = __all_sync(0xffffffffu, mbar_wait(b_acc, 0));
       if (good) {
         drain([&](int t, int g, int v) {
           const int slot = t >> shift, owner = t & (split - 1);
@@ -278,7 +278,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   } else {
     if (warp >= 2) {
       int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
-      if (mbar_wait(b_acc, 0)) drain([&](int t, int g, int v) { sums[(t * NW + g) * kRows + ch] = v; });
+      if (__all_sync(0xffffffffu, mbar_wait(b_acc, 0))) drain([&](int t, int g, int v) { sums[(t * NW + g) * kRows + ch] = v; });
       else fail();
     }
     // a CTA whose wait gave up has no sums: nobody of its cluster writes then

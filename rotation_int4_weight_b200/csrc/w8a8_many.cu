@@ -160,6 +160,7 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     const bool by_tma = (A.d_out & 7) == 0;
     const uint32_t lanes = tmem + ((uint32_t)(quarter * 32) << 16);
     int j = 0, turn = 0;
+    bool ok = true;  // the same in all lanes; a warp that gave up still meets the others at their barriers
 #pragma unroll 1
     for (int t = pair; t < A.tiles; t += pairs, ++j) {
       const int acc = j & 1;
@@ -174,7 +175,9 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         if constexpr (!GATED) s_bias[acc][c] = A.bias && n < A.d_out ? from_16<F16>(A.bias[n]) : 0.0f;
       }
       asm volatile("bar.sync 1, %0;\n" ::"n"(32 * kEpiWarps) : "memory");
-      if (!wait(b_acc_full + 8 * acc, (j >> 1) & 1)) { fail(); break; }
+      if (!ok) continue;
+      ok = __all_sync(0xffffffffu, wait(b_acc_full + 8 * acc, (j >> 1) & 1));
+      if (!ok) { fail(); continue; }
       tc_fence_after();
 #pragma unroll 1
       for (int c0 = half * (NC / 2); c0 < (half + 1) * (NC / 2) && n0 + c0 < A.d_out; c0 += 32) {
