@@ -511,6 +511,59 @@ def test_offsets_beyond_32_bits():
     assert_linear(y[rows], q[rows], sx[rows], w, sw)
 
 
+def test_more_token_tiles_than_a_grid_has_rows():
+    # beyond 65535 tiles of 128 tokens (64 for a gated pair): only the kernel for many tokens takes them
+    M, d_in, d_out = 65535 * 128 + 3, 16, 5
+    q, sx, w, sw, w2, s2, b = _operands(M, d_in, d_out, 4)
+    rows = torch.cat([torch.arange(300, device=DEV), torch.arange(0, M, 4099, device=DEV),
+                      torch.arange(M - 300, M, device=DEV)])
+    y = paro.paro_w8a8_linear(q, sx, w, sw, b.to(BF16))
+    _status_ok()
+    assert_linear(y[rows], q[rows], sx[rows], w, sw, b.to(BF16))
+    y = paro.paro_w8a8_swiglu(q, sx, w, sw, w2, s2)
+    _status_ok()
+    assert_swiglu(y[rows], q[rows], sx[rows], w, sw, w2, s2)
+
+
+@pytest.mark.parametrize("M,d_out", [(8, 1536), (100, 520), (1100, 2049)])
+def test_scales_that_are_not_finite_void_their_rows_and_channels_only(M, d_out):
+    q, sx, w, sw, _, _, _ = _operands(M, 528, d_out, 5)
+    alone = paro.paro_w8a8_linear(q, sx, w, sw)
+    sx2, sw2 = sx.clone(), sw.clone()
+    sx2[[0, M - 1]], sw2[[3, d_out - 1]] = float("nan"), float("nan")
+    y = paro.paro_w8a8_linear(q, sx2, w, sw2)
+    _status_ok()
+    bad = torch.isnan(sx2)[:, None] | torch.isnan(sw2)[None, :]
+    assert torch.isnan(y[bad]).all() and torch.equal(y[~bad], alone[~bad])
+
+
+def test_calls_from_two_threads():
+    import threading
+    sets = [_operands(M, 2064, 1100, M)[:4] for M in (3, 700)]
+    alone = [paro.paro_w8a8_linear(*s) for s in sets]
+    torch.cuda.synchronize()
+    got, errors = [[], []], []
+
+    def work(k):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                got[k] = [paro.paro_w8a8_linear(*sets[k]) for _ in range(50)]
+            s.synchronize()
+        except Exception as e:
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(k,)) for k in (0, 1)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for k in (0, 1):
+        assert len(got[k]) == 50 and all(torch.equal(y, alone[k]) for y in got[k])
+    _status_ok()
+
+
 def test_refusals():
     q = torch.zeros(2, 64, dtype=torch.int8, device=DEV)
     s, w, sw = torch.ones(2, device=DEV), torch.zeros(8, 64, dtype=torch.int8, device=DEV), torch.ones(8, device=DEV)
