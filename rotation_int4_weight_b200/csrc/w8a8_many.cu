@@ -164,7 +164,7 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
 #pragma unroll 1
     for (int t = pair; t < A.tiles; t += pairs, ++j) {
       const int acc = j & 1;
-      const int m = (t % A.mtiles) * kTile + rank * kHalf + quarter * 32 + lane, n0 = (t / A.mtiles) * NC;
+      const int m_warp = (t % A.mtiles) * kTile + rank * kHalf + quarter * 32, m = m_warp + lane, n0 = (t / A.mtiles) * NC;
       const float sx = m < A.M ? A.sx[m] : 0.0f;
       // the tile's channel values, while its MMAs run; two sets, so that a warp
       // may be one tile ahead of another
@@ -179,8 +179,11 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       ok = __all_sync(0xffffffffu, wait(b_acc_full + 8 * acc, (j >> 1) & 1));
       if (!ok) { fail(); continue; }
       tc_fence_after();
+      // (none where all of the warp's tokens lie behind the last one: every use of a
+      // box below commits one store, which the wait two uses later counts on)
+      const int c_end = m_warp < A.M ? min((half + 1) * (NC / 2), A.d_out - n0) : 0;
 #pragma unroll 1
-      for (int c0 = half * (NC / 2); c0 < (half + 1) * (NC / 2) && n0 + c0 < A.d_out; c0 += 32) {
+      for (int c0 = half * (NC / 2); c0 < c_end; c0 += 32) {
         int v[32], u[GATED ? 32 : 1];
         tmem_ld(lanes + acc * kTile + c0, v);
         if constexpr (GATED) tmem_ld(lanes + acc * kTile + kHalf + c0, u);
@@ -214,11 +217,10 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-        const int m_warp = m - lane;
         if (by_tma) {
           async_fence();
           __syncwarp();
-          if (lane == 0 && m_warp < A.M) {
+          if (lane == 0) {
             tma_store(&A.out, smem_u32(box), n, m_warp);
             bulk_commit();
           }
