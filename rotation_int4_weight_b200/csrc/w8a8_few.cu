@@ -136,10 +136,11 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     if (lane == 0) {
       int i = 0, s = 0, x = k0 * kK;
       uint32_t phase = 1, dst = ring, bar = b_full;
+      bool ok = true;
 #pragma unroll 1
       for (; i < nk; ++i, x += kK) {
         // (phase starts at 1: the first wait, a round later, is for parity 0)
-        if (i >= stages && !wait(bar + (b_empty - b_full), phase)) { fail(); break; }
+        if (i >= stages && !wait(bar + (b_empty - b_full), phase)) { fail(); ok = false; break; }
         mbar_expect_tx(bar, (NW * kRows + A.xrows) * kK);
         tma_load(dst, &A.w, x, n0, bar);
         if constexpr (GATED) tma_load(dst + kRows * kK, &A.w2, x, n0, bar);
@@ -148,6 +149,9 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
         else dst += Geo::STAGE, bar += 8;
       }
       s_issued = i;
+      // the last stages' commits have arrived before the CTA, and the barriers with it, may go
+      for (int j = i > stages ? i - stages : 0; ok && j < i; ++j)
+        if (!wait(b_empty + 8 * (j % stages), (j / stages) & 1)) { fail(); ok = false; }
     }
   } else if (warp == 1) {
     if (lane == 0) {

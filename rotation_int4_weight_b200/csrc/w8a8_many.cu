@@ -128,6 +128,9 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         }
       }
       s_issued = it;
+      // the last stages' commits have arrived before this CTA, and its barriers with it, may go
+      for (int i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
+        if (!wait(b_empty + 8 * (i % kStages), (i / kStages) & 1)) { fail(); ok = false; }
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
