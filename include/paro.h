@@ -489,14 +489,19 @@ PARO_API paro_status paro_get_device_status(paro_stream_t stream);
  * how later launches are configured and stay set until called again.
  * flag_wait_cycles > 0 bounds every wait of the decode INT4 kernel for a
  * hand-over flag (the transform's "x~ is written" flags, and the partial
- * sums of a tile split between CTAs) to about that many SM clock cycles
- * instead of about 2^31 (a second); 0 restores the default.
+ * sums of a tile split between CTAs), and every wait of the int8 linears'
+ * roles for one another, to about that many SM clock cycles instead of about
+ * 2^31 (a second); 0 restores the default.
  * skip_ready_flags != 0 makes the decode transforms (in the fused one-token
  * launch and in the transform launch before the INT4 launch at 2-16 tokens)
  * skip publishing their "x~ is written" flags, so that the INT4 kernel's
  * waits run out: the call then reports PARO_ERR_TIMEOUT through
  * paro_get_device_status() and writes none of the output tiles of the linears
- * it waited for.  Nothing hangs: every wait is bounded.  Not thread-safe with
+ * it waited for.  In the int8 linears it makes the last CTA of every cluster
+ * (the first, where skip_ready_flags is 2) stop its copies after the first 128
+ * columns of its share of d_in, so that the waits for the others run out: the
+ * call reports PARO_ERR_TIMEOUT and writes no tile that such a CTA has a share
+ * in, if that share is longer.  Nothing hangs: these waits are bounded.  Not thread-safe with
  * respect to calls being configured at the same time; PARO_ERR_INVALID_ARG
  * for a negative cycle count.
  */

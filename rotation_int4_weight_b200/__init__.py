@@ -434,12 +434,14 @@ def paro_plan_pair_order(pairs, cos_t, sin_t):
     return po, co, so
 
 
-def paro_set_test_hooks(flag_wait_cycles: int = 0, skip_ready_flags: bool = False) -> None:
+def paro_set_test_hooks(flag_wait_cycles: int = 0, skip_ready_flags: bool | int = False) -> None:
     """Test hooks of the failure paths: bound the decode INT4 kernel's hand-over
-    flag waits to `flag_wait_cycles` SM cycles (0: the default, about a second)
-    and make the decode transforms skip publishing their flags.  Affects the
-    calls configured afterwards; (0, False) restores the defaults."""
-    _check(lib.paro_set_test_hooks(int(flag_wait_cycles), 1 if skip_ready_flags else 0), "paro_set_test_hooks")
+    flag waits and the int8 linears' waits to `flag_wait_cycles` SM cycles (0: the
+    default, about a second), make the decode transforms skip publishing their
+    flags, and make the last CTA of every cluster of the int8 linears (2: the
+    first) stop copying after one step.  Affects the calls configured afterwards;
+    (0, False) restores the defaults."""
+    _check(lib.paro_set_test_hooks(int(flag_wait_cycles), int(skip_ready_flags or 0)), "paro_set_test_hooks")
 
 
 def paro_get_device_status(stream=None) -> int:

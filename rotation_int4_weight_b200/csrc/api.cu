@@ -224,7 +224,7 @@ const char* paro_last_error(void) { return t_last_error; }
 paro_status paro_set_test_hooks(long long flag_wait_cycles, int skip_ready_flags) {
   if (flag_wait_cycles < 0) return fail(PARO_ERR_INVALID_ARG, "flag_wait_cycles = %lld is negative", flag_wait_cycles);
   g_hook_flag_wait.store(flag_wait_cycles, std::memory_order_relaxed);
-  g_hook_skip_flags.store(skip_ready_flags != 0 ? 1 : 0, std::memory_order_relaxed);
+  g_hook_skip_flags.store(skip_ready_flags, std::memory_order_relaxed);
   return ok();
 }
 

@@ -35,8 +35,9 @@ __device__ __forceinline__ void report_status(int* status, int code) {
 // Stores a printf-style message for paro_last_error() and returns s.
 paro_status record_error(paro_status s, const char* fmt, ...);
 
-// Test hooks (paro_set_test_hooks): the wait bound for hand-over flags in
-// cycles, and whether the decode transforms skip publishing their flags.
+// Test hooks (paro_set_test_hooks): the bound of waits for hand-over flags, and of
+// the int8 linears' waits, in cycles; whether the decode transforms skip publishing
+// their flags and CTAs of the int8 linears stop copying (0: no).
 long long hook_flag_wait();
 int hook_skip_ready_flags();
 

@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paro_internal.cuh"  // kWaitCycles
+
 namespace paro {
 namespace ptx {
 
@@ -39,21 +41,21 @@ __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
 }
-// Bounded wait on an mbarrier phase (about a second of SM clock).
-__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
+// Wait on an mbarrier phase, given up (false) after `limit` SM clocks.
+__device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, long long limit = kWaitCycles) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_test(bar, parity))
-    if (clock64() - t0 > (1LL << 31)) return false;
+    if (clock64() - t0 > limit) return false;
   return true;
 }
 
-// The same, given up (false) when *stop is set, too.
-__device__ __forceinline__ bool mbar_wait_unless(uint32_t bar, uint32_t parity, const int* stop) {
+// The same, given up when *stop is set, too.
+__device__ __forceinline__ bool mbar_wait_unless(uint32_t bar, uint32_t parity, const int* stop, long long limit) {
   if (mbar_test(bar, parity)) return true;
   const long long t0 = clock64();
   while (!mbar_test(bar, parity))
-    if (*(const volatile int*)stop != 0 || clock64() - t0 > (1LL << 31)) return false;
+    if (*(const volatile int*)stop != 0 || clock64() - t0 > limit) return false;
   return true;
 }
 

@@ -63,6 +63,11 @@ cudaError_t allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& don
   return e;
 }
 
+W8a8Hooks w8a8_hooks(int cluster) {
+  const int skip = hook_skip_ready_flags();
+  return {hook_flag_wait(), skip == 0 ? -1 : skip == 2 ? 0 : cluster - 1};
+}
+
 // The kernel with the smaller estimate, both fits to measured times (bf16, GPU time
 // of calls in a row, weights from HBM).  The kernel for many tokens takes 0.35 us
 // per 128 columns and round of tiles (256 x 256 on a pair of SMs) and 5.6 us around

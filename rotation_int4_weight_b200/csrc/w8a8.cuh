@@ -16,6 +16,15 @@ struct W8a8Few {
 };
 W8a8Few w8a8_few_shape(const W8a8Args& a);
 
+// What paro_set_test_hooks changes of a launch: the SM clocks after which a role's
+// wait on an mbarrier gives up, and the CTA of every cluster whose copies stop after
+// the first stage (-1: none).
+struct W8a8Hooks {
+  long long wait;
+  int rank;
+};
+W8a8Hooks w8a8_hooks(int cluster);
+
 // The two kernels of launch_w8a8.
 cudaError_t launch_w8a8_few(const W8a8Args& a, const W8a8Few& f, int* status, cudaStream_t stream);
 cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream);

@@ -28,6 +28,10 @@
 // The launch overlaps the kernel before it: until that one is done a CTA sets up
 // its barriers and asks for its weights in L2 only, which is right whoever wrote
 // them last; every read and write of its own comes after the wait.
+//
+// Every wait on an mbarrier is bounded: when one runs out, the CTA's roles end, its
+// copies and MMAs in flight are waited for, no CTA writes what it has no sums of, and
+// the call reports PARO_ERR_TIMEOUT.
 #include <climits>
 
 #include "int8.cuh"
@@ -51,13 +55,15 @@ constexpr int kAhead = 2;
 
 struct FewArgs {
   CUtensorMap w, w2, q;
+  // in front: what the first copies wait for is in one line of the constant cache
+  W8a8Hooks hooks;
+  int M, d_out, blocks;      // blocks: of 128 columns of d_in
+  int split, stages, xrows;  // xrows: tokens a copy brings, at most TN
   const float* sx;
   const float* sw;
   const float* sw2;
   const uint16_t* bias;
   uint16_t* y;
-  int M, d_out, blocks;  // blocks: of 128 columns of d_in
-  int split, stages, xrows;  // xrows: tokens a copy brings, at most TN
 };
 
 template <int TN, bool GATED>
@@ -126,7 +132,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
     atomicExch(&abort_flag, 1);
   };
   // a wait that also ends, false, when another role gave up
-  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag, A.hooks.wait); };
 
   // The two loops below set the pace: each step of one thread costs 280 clocks and
   // up (waits, barrier, copies), so stages and parities are counted, not divided,
@@ -134,11 +140,12 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   // 800 clocks, which held every SM to 40 GB/s.
   if (warp == 0) {
     if (lane == 0) {
+      const int copied = rank == A.hooks.rank && nk > 1 ? 1 : nk;
       int i = 0, s = 0, x = k0 * kK;
       uint32_t phase = 1, dst = ring, bar = b_full;
       bool ok = true;
 #pragma unroll 1
-      for (; i < nk; ++i, x += kK) {
+      for (; i < copied; ++i, x += kK) {
         // (phase starts at 1: the first wait, a round later, is for parity 0)
         if (i >= stages && !wait(bar + (b_empty - b_full), phase)) { fail(); ok = false; break; }
         mbar_expect_tx(bar, (NW * kRows + A.xrows) * kK);
@@ -150,8 +157,11 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
       }
       s_issued = i;
       // the last stages' commits have arrived before the CTA, and the barriers with it, may go
-      for (int j = i > stages ? i - stages : 0; ok && j < i; ++j)
-        if (!wait(b_empty + 8 * (j % stages), (j / stages) & 1)) { fail(); ok = false; }
+      if (i < stages) s = 0, phase = 0;
+      for (int n = i < stages ? i : stages; ok && n > 0; --n) {
+        if (!wait(b_empty + 8 * s, phase)) { fail(); ok = false; }
+        if (++s == stages) s = 0, phase ^= 1;
+      }
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -256,7 +266,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
       // [share][its slot of the owner's tokens][NW][128]
       const uint32_t sums = ring + stages * Geo::STAGE;
       const int shift = 31 - __clz(split), slots = (tokens + split - 1) >> shift;  // split: a power of two
-      const bool good = __all_sync(0xffffffffu, mbar_wait(b_acc, 0));
+      const bool good = __all_sync(0xffffffffu, mbar_wait(b_acc, 0, A.hooks.wait));
       if (good) {
         drain([&](int t, int g, int v) {
           const int slot = t >> shift, owner = t & (split - 1);
@@ -268,7 +278,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
         fail();
       }
       if (rank < tokens) {
-        if (good && mbar_wait(b_sums, 0)) {
+        if (good && mbar_wait(b_sums, 0, A.hooks.wait)) {
           const int4* from = reinterpret_cast<const int4*>(smem + stages * Geo::STAGE) + lane;
 #pragma unroll 2
           for (int t = rank + split * (warp - 2); t < tokens; t += split * 4)
@@ -282,7 +292,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   } else {
     if (warp >= 2) {
       int* sums = reinterpret_cast<int*>(smem);  // [token][NW][128]
-      if (__all_sync(0xffffffffu, mbar_wait(b_acc, 0))) drain([&](int t, int g, int v) { sums[(t * NW + g) * kRows + ch] = v; });
+      if (__all_sync(0xffffffffu, mbar_wait(b_acc, 0, A.hooks.wait))) drain([&](int t, int g, int v) { sums[(t * NW + g) * kRows + ch] = v; });
       else fail();
     }
     // a CTA whose wait gave up has no sums: nobody of its cluster writes then
@@ -355,6 +365,7 @@ cudaError_t launch_few(FewArgs& A, const W8a8Few& f, int* status, cudaStream_t s
   if (Geo::STORED) bytes += Geo::SUMS;
   else if (bytes < Geo::SUMS) bytes = Geo::SUMS;
   A.stages = stages;
+  A.hooks = w8a8_hooks(f.split);
   bytes += 1024;
   auto kernel = w8a8_few_kernel<TN, GATED, F16>;
   static std::atomic<uint64_t> limit{0};

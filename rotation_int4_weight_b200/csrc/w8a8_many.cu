@@ -19,7 +19,11 @@
 // 2048 tokens 14336 -> 4096 in 84.5 us (2.85 PFLOP/s; 99 us when it runs for
 // seconds), gated 4096 -> 14336 in 164 us (2.93).
 // Two sets of sums (2 x 256 columns of tensor memory) let the next tile's MMAs
-// run under a tile's epilogue.  Every wait is bounded.
+// run under a tile's epilogue.  Every wait on an mbarrier is bounded; when one runs
+// out, the roles of both CTAs end, their copies and MMAs in flight are waited for,
+// and the call reports PARO_ERR_TIMEOUT.
+#include <climits>
+
 #include "int8.cuh"
 #include "tc_ptx.cuh"
 #include "w4_stream.cuh"  // device_sm_count
@@ -49,6 +53,7 @@ struct ManyArgs {
   uint16_t* y;
   int M, d_out, blocks;  // blocks: of 128 columns of d_in
   int mtiles, tiles;
+  W8a8Hooks hooks;
 };
 
 template <bool GATED, bool F16>
@@ -101,7 +106,7 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     atomicExch(&abort_flag, 1);
   };
   // a wait that also ends, false, when another role gave up
-  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag); };
+  auto wait = [&](uint32_t bar, uint32_t parity) { return mbar_wait_unless(bar, parity, &abort_flag, A.hooks.wait); };
 
   // One thread's step (wait, barrier, copies or MMAs) has to stay below the 512
   // clocks that a stage's MMAs take: stages and parities are counted, and the abort
@@ -113,12 +118,13 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       int it = 0, s = 0;
       uint32_t phase = 1;
       bool ok = true;
+      const int copied = rank == A.hooks.rank ? 1 : INT_MAX;
 #pragma unroll 1
-      for (int t = pair; ok && t < A.tiles; t += pairs) {
+      for (int t = pair; ok && it < copied && t < A.tiles; t += pairs) {
         const int m0 = (t % A.mtiles) * kTile + rank * kHalf;
         const int n0 = (t / A.mtiles) * NC + (GATED ? 0 : rank * kHalf);
 #pragma unroll 1
-        for (int x = 0; x < A.blocks * kK; x += kK, ++it) {
+        for (int x = 0; x < A.blocks * kK && it < copied; x += kK, ++it) {
           if (it >= kStages && !wait(b_empty + 8 * s, phase)) { fail(); ok = false; break; }
           const uint32_t bar = first + 8 * s, dst = ring + s * kStageBytes;
           if (rank == 0) mbar_expect_tx(b_full + 8 * s, 2 * kStageBytes);
@@ -129,8 +135,11 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       }
       s_issued = it;
       // the last stages' commits have arrived before this CTA, and its barriers with it, may go
-      for (int i = it > kStages ? it - kStages : 0; ok && i < it; ++i)
-        if (!wait(b_empty + 8 * (i % kStages), (i / kStages) & 1)) { fail(); ok = false; }
+      if (it < kStages) s = 0, phase = 0;
+      for (int n = it < kStages ? it : kStages; ok && n > 0; --n) {
+        if (!wait(b_empty + 8 * s, phase)) { fail(); ok = false; }
+        if (++s == kStages) s = 0, phase ^= 1;
+      }
     }
   } else if (warp == 1) {
     if (rank == 0 && lane == 0) {
@@ -323,6 +332,7 @@ cudaError_t launch_w8a8_many(const W8a8Args& a, int* status, cudaStream_t stream
   A.M = a.M;
   A.d_out = a.d_out;
   A.blocks = (a.d_in + kK - 1) / kK;
+  A.hooks = w8a8_hooks(2);
   A.mtiles = (a.M + kTile - 1) / kTile;
   const int nc = a.w2 ? kHalf : kTile;
   A.tiles = A.mtiles * ((a.d_out + nc - 1) / nc);
