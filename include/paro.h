@@ -299,6 +299,14 @@ PARO_API paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, cons
                                       paro_dtype dtype, paro_stream_t stream);
 
 /*
+ * Host-side: how paro_w8a8_linear (paro_w8a8_swiglu with gated != 0) cuts a call of
+ * this shape on the current device: form[0] and form[1] the tokens and output
+ * channels of a tile (256 tokens: the kernel for many tokens on pairs of SMs, fewer:
+ * the one for few tokens), form[2] the shares of d_in.  y does not depend on it.
+ */
+PARO_API paro_status paro_w8a8_form(int M, int d_in, int d_out, int gated, int* form);
+
+/*
  * The whole 8-bit path of one transformed linear: the activation transform (as
  * paro_rotate, bf16 x~ into the workspace), its row codes and the int8 linear on
  * weights of paro_pack_weights_int8, three launches on `stream`, bf16 in and out.

@@ -22,7 +22,7 @@ __all__ = [
     "paro_rotate_backward_workspace_bytes", "paro_rotate_backward", "paro_set_test_hooks", "paro_dense_rotate",
     "paro_quantize_activations", "paro_w4a4_linear", "paro_rotate_w4a4_linear",
     "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
-    "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear",
+    "paro_w8a8_swiglu", "paro_w8a8_form", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear",
 ]
 
 # PARO_TIMELINE=1 loads the instrumented build (same kernels plus global-timer
@@ -59,6 +59,7 @@ EXPORTED = {
     "paro_pack_weights_int8": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P]),
     "paro_w8a8_linear": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
     "paro_w8a8_swiglu": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _P]),
+    "paro_w8a8_form": (_I, [_I, _I, _I, _I, _P]),
     "paro_rotate_w8a8_workspace_bytes": (_S, [_I, _I]),
     "paro_rotate_w8a8_linear": (_I, [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _S, _P]),
 }
@@ -329,6 +330,14 @@ def paro_w8a8_swiglu(q: torch.Tensor, sx, gate_qweight, gate_wscales, up_qweight
         if r is not NotImplemented:
             return r
     return _elsewhere(_binding.swiglu, stream, q, sx, gate_qweight, gate_wscales, up_qweight, up_wscales, out, out_dtype)
+
+
+def paro_w8a8_form(M: int, d_in: int, d_out: int, gated: bool = False):
+    """How an int8 linear of this shape is cut on the current device: (tokens of a tile, channels of a
+    tile, shares of d_in); 256 tokens are the kernel for many tokens, fewer the one for few."""
+    form = (_I * 3)()
+    _check(lib.paro_w8a8_form(M, d_in, d_out, 1 if gated else 0, form), "paro_w8a8_form")
+    return tuple(form)
 
 
 def paro_rotate_w8a8_workspace_bytes(M: int, d_in: int) -> int:

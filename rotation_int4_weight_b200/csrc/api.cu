@@ -962,6 +962,18 @@ paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t*
                   dtype, stream);
 }
 
+paro_status paro_w8a8_form(int M, int d_in, int d_out, int gated, int* form) {
+  paro_status st;
+  if (M <= 0) return fail(PARO_ERR_INVALID_ARG, "M = %d must be positive", M);
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK) return st;
+  if (M > kMaxW8Rows || d_out > kMaxW8Rows)
+    return fail(PARO_ERR_UNSUPPORTED, "M = %d or d_out = %d exceeds %d", M, d_out, kMaxW8Rows);
+  if (!form) return fail(PARO_ERR_INVALID_ARG, "null pointer");
+  const paro::W8a8Form f = paro::w8a8_form(M, d_in, d_out, gated != 0);
+  form[0] = f.tokens, form[1] = f.channels, form[2] = f.shares;
+  return ok();
+}
+
 size_t paro_rotate_w8a8_workspace_bytes(int M, int d_in) {
   if (M <= 0 || d_in <= 0) return 0;
   return r256((size_t)M * d_in * 2) + r256((size_t)M * d_in) + r256((size_t)M * 4);

@@ -38,5 +38,11 @@ struct W8a8Args {
   bool f16;              // y and bias: fp16, else bf16
 };
 cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream);
+// How that call is cut: tokens and channels of a tile (256 tokens: w8a8_many.cu,
+// else w8a8_few.cu) and the shares of d_in.
+struct W8a8Form {
+  int tokens, channels, shares;
+};
+W8a8Form w8a8_form(int M, int d_in, int d_out, bool gated);
 
 }  // namespace paro

@@ -78,13 +78,27 @@ W8a8Hooks w8a8_hooks(int cluster) {
 //   1552 -> 1100:  M 203: 6.5 / 12;
 //   gated 1536 -> 8960: M 33: 11 / 14, M 129: 21 / 11.9;
 //   gated 14336 -> 4096: M 128: 33.8 / 45, M 129: 52 / 45.
-cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream) {
-  const W8a8Few f = w8a8_few_shape(a);
+static bool takes_few(const W8a8Args& a, const W8a8Few& f) {
   const long long blocks = (a.d_in + 127) / 128, pairs = device_sm_count() / 2;
   const int nc = a.w2 ? 128 : 256;
   const long long tiles = ((a.M + 255LL) / 256) * ((a.d_out + nc - 1) / nc);
   const long long many = 5600 + (a.d_out % 8 ? 4000 : 0) + (tiles + pairs - 1) / pairs * blocks * 350;
-  return a.M <= 32 || f.ns <= many ? launch_w8a8_few(a, f, status, stream) : launch_w8a8_many(a, status, stream);
+  return a.M <= 32 || f.ns <= many;
+}
+
+cudaError_t launch_w8a8(const W8a8Args& a, int* status, cudaStream_t stream) {
+  const W8a8Few f = w8a8_few_shape(a);
+  return takes_few(a, f) ? launch_w8a8_few(a, f, status, stream) : launch_w8a8_many(a, status, stream);
+}
+
+W8a8Form w8a8_form(int M, int d_in, int d_out, bool gated) {
+  W8a8Args a{};
+  const int8_t some = 0;
+  a.w2 = gated ? &some : nullptr;
+  a.M = M, a.d_in = d_in, a.d_out = d_out;
+  const W8a8Few f = w8a8_few_shape(a);
+  if (takes_few(a, f)) return {f.tokens, 128, f.split};
+  return {256, gated ? 128 : 256, 1};
 }
 
 }  // namespace paro

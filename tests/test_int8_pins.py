@@ -183,3 +183,31 @@ def test_binding_refuses_what_the_library_cannot_see():
         paro.paro_w8a8_linear(q, s, q, s)
     with pytest.raises(ValueError, match="bfloat16 or float16"):
         paro.paro_w8a8_linear(q, s, q, s, out_dtype=torch.float32)
+
+
+# ------------------------------------------------------------------ the linears' forms
+def test_w8a8_form_validation():
+    form = (ctypes.c_int * 3)()
+    call = paro.lib.paro_w8a8_form
+    assert call(1, 512, 100, 0, form) == OK and list(form) == [16, 128, 4]
+    for bad in ((0, 512, 100, 0, form), (-1, 512, 100, 0, form), (1, 500, 100, 0, form), (1, 512, 0, 0, form),
+                (1, 512, 100, 0, None)):
+        assert call(*bad) == INVALID
+    assert call(1, 49168, 100, 0, form) == UNSUPPORTED
+    assert call((1 << 30) + 1, 16, 1, 1, form) == UNSUPPORTED
+
+
+def test_every_form_of_the_int8_linears_is_compared_with_the_exact_product():
+    # the shapes of test_gpu_int8_forms.py reach every form that any shape does, so that
+    # new constants of the choice cannot leave a kernel without a test
+    from tests.test_gpu_int8_forms import FORMS
+    key = lambda M, d_in, d_out, gated: (gated,) + paro.paro_w8a8_form(M, d_in, d_out, gated)
+    for shape, form in FORMS.items():
+        assert key(*shape)[1:] == form, shape
+    rng = np.random.default_rng(6)
+    u = rng.random((60000, 3))
+    seen = set()
+    for a, b, c in u:
+        M, d_in, d_out = int(8192 ** a), 16 * int(3072 ** b), int(60000 ** c)
+        seen |= {key(M, d_in, d_out, g) for g in (0, 1)}
+    assert seen == {key(*s) for s in FORMS}, seen ^ {key(*s) for s in FORMS}
