@@ -842,12 +842,18 @@ paro_status check_w8_weights(const int8_t* w, const float* s) {
 
 constexpr int kMaxW8Rows = 1 << 30;  // tile coordinates stay within 31 bits
 
+paro_status check_w8_rows(int M, int d_out) {
+  if (M > kMaxW8Rows || d_out > kMaxW8Rows)
+    return fail(PARO_ERR_UNSUPPORTED, "M = %d or d_out = %d exceeds %d", M, d_out, kMaxW8Rows);
+  return PARO_OK;
+}
+
 // Checks and launches both int8 linears (d_w2 and d_s2 null: the plain one).
 paro_status run_w8a8(const int8_t* d_q, const float* d_sx, const int8_t* d_w, const float* d_s, const int8_t* d_w2,
                      const float* d_s2, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in, int d_out,
                      paro_dtype dtype, paro_stream_t stream) {
-  if (M > kMaxW8Rows || d_out > kMaxW8Rows)
-    return fail(PARO_ERR_UNSUPPORTED, "M = %d or d_out = %d exceeds %d", M, d_out, kMaxW8Rows);
+  paro_status st;
+  if ((st = check_w8_rows(M, d_out)) != PARO_OK) return st;
   if (!d_q || !d_sx || !d_y) return fail(PARO_ERR_INVALID_ARG, "null activation pointer");
   if (!aligned(d_q, 16) || !aligned(d_sx, 4) || !aligned(d_y, 16))
     return fail(PARO_ERR_INVALID_ARG, "q and y must be 16-byte aligned, sx 4-byte");
@@ -965,9 +971,7 @@ paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t*
 paro_status paro_w8a8_form(int M, int d_in, int d_out, int gated, int* form) {
   paro_status st;
   if (M <= 0) return fail(PARO_ERR_INVALID_ARG, "M = %d must be positive", M);
-  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK) return st;
-  if (M > kMaxW8Rows || d_out > kMaxW8Rows)
-    return fail(PARO_ERR_UNSUPPORTED, "M = %d or d_out = %d exceeds %d", M, d_out, kMaxW8Rows);
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK || (st = check_w8_rows(M, d_out)) != PARO_OK) return st;
   if (!form) return fail(PARO_ERR_INVALID_ARG, "null pointer");
   const paro::W8a8Form f = paro::w8a8_form(M, d_in, d_out, gated != 0);
   form[0] = f.tokens, form[1] = f.channels, form[2] = f.shares;
@@ -985,7 +989,7 @@ paro_status paro_rotate_w8a8_linear(const uint16_t* d_x, int K, const uint16_t* 
                                     int d_out, void* d_workspace, size_t workspace_bytes, paro_stream_t stream) {
   paro_status st;
   if (M < 0) return fail(PARO_ERR_INVALID_ARG, "M = %d is negative", M);
-  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK) return st;
+  if ((st = check_w8_shape(d_in, d_out)) != PARO_OK || (st = check_w8_rows(M, d_out)) != PARO_OK) return st;
   if ((st = check_tables(K, d_in, d_pairs, d_cos, d_sin, d_scale)) != PARO_OK) return st;
   if (M == 0) return ok();
   if ((st = check_w8_weights(d_qweight, d_wscales)) != PARO_OK) return st;

@@ -160,6 +160,17 @@ def test_rotate_w8a8_validation(change, expect):
     assert st == expect, paro.lib.paro_last_error()
 
 
+@pytest.mark.parametrize("change", [dict(M=(1 << 30) + 1), dict(d_out=(1 << 30) + 1)])
+def test_rotate_w8a8_refuses_sizes_before_it_enqueues(change):
+    # the linear's limit on rows is looked at before the transform is launched (which, without
+    # a GPU, would be the first to fail); pointers 1 TB apart, never dereferenced
+    at = lambda i: ctypes.c_void_p(i << 40)
+    a = dict(M=4, d_out=100) | change
+    st = paro.lib.paro_rotate_w8a8_linear(at(1), 8, at(2), at(3), at(4), None, at(5), at(6), None, at(7), a["M"], 16,
+                                          a["d_out"], at(8), 1 << 40, None)
+    assert st == UNSUPPORTED, paro.lib.paro_last_error()
+
+
 def test_rotate_w8a8_workspace_bytes():
     r = lambda b: (b + 255) // 256 * 256
     for M, d in [(1, 16), (3, 1536), (2048, 4096)]:
