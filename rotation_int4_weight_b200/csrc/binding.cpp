@@ -165,8 +165,14 @@ PyObject* output(PyObject* t, PyObject* dtype, int n, const long long* sizes, in
   return addressed(PyObject_Vectorcall(f_empty, args, k, k_empty), out);
 }
 
-// Raises ParoError for a status that is not OK.
-bool done(paro_status st, const char* what) {
+// Calls the library, with the interpreter's lock given up (a launch may wait for
+// room in the stream's queue), and raises ParoError for a status that is not OK.
+template <typename F, typename... A>
+bool run(const char* what, F fn, A... args) {
+  paro_status st;
+  Py_BEGIN_ALLOW_THREADS
+  st = fn(args...);
+  Py_END_ALLOW_THREADS
   if (st == PARO_OK) return true;
   Ref r(PyObject_CallFunction(f_check, "is", (int)st, what));
   if (r.p) PyErr_SetString(PyExc_RuntimeError, what);
@@ -197,7 +203,7 @@ PyObject* quantize(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (!oq.p) return nullptr;
   Ref os(output(v[2], t_f32, 1, d, dev, v[0], "sx", &sx));
   if (!os.p || !stream_of(dev, &s)) return nullptr;
-  if (!done(api.quantize((uint16_t*)x, (int8_t*)q, (float*)sx, (int)d[0], (int)d[1], ty, s), "paro_quantize_activations_int8"))
+  if (!run("paro_quantize_activations_int8", api.quantize, (uint16_t*)x, (int8_t*)q, (float*)sx, (int)d[0], (int)d[1], ty, s))
     return nullptr;
   return PyTuple_Pack(2, oq.p, os.p);
 }
@@ -230,9 +236,8 @@ PyObject* norm(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (!oq.p) return nullptr;
   Ref os(output(v[6], t_f32, 1, d, dev, v[0], "sx", &sx));
   if (!os.p || !stream_of(dev, &s)) return nullptr;
-  if (!done(api.norm((uint16_t*)x, (uint16_t*)r, (uint16_t*)g, (float)eps, (uint16_t*)h, (int8_t*)q, (float*)sx, (int)d[0],
-                     (int)d[1], ty, s),
-            "paro_rms_norm_int8"))
+  if (!run("paro_rms_norm_int8", api.norm, (uint16_t*)x, (uint16_t*)r, (uint16_t*)g, (float)eps, (uint16_t*)h, (int8_t*)q,
+           (float*)sx, (int)d[0], (int)d[1], ty, s))
     return nullptr;
   return PyTuple_Pack(3, oq.p, os.p, oh.p);
 }
@@ -275,9 +280,8 @@ PyObject* pack(PyObject*, PyObject* const* v, Py_ssize_t n) {
   if (!oq.p) return nullptr;
   Ref os(output(v[7], t_f32, 1, d, dev, v[0], "wscales", &ss));
   if (!os.p || !stream_of(dev, &s)) return nullptr;
-  if (!done(api.pack((float*)W, (int)d[0], (int)d[1], (int)t.K, (uint16_t*)t.pairs, (float*)t.cos, (float*)t.sin,
-                     (float*)t.scale, (float*)ws, (int8_t*)q, (float*)ss, s),
-            "paro_pack_weights_int8"))
+  if (!run("paro_pack_weights_int8", api.pack, (float*)W, (int)d[0], (int)d[1], (int)t.K, (uint16_t*)t.pairs, (float*)t.cos,
+           (float*)t.sin, (float*)t.scale, (float*)ws, (int8_t*)q, (float*)ss, s))
     return nullptr;
   return PyTuple_Pack(2, oq.p, os.p);
 }
@@ -313,10 +317,11 @@ PyObject* linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
   Ref oy(output(v[O], t.p, 2, ysize, dev, v[0], "out", &y));
   if (!oy.p || !stream_of(dev, &s)) return nullptr;
   const int M = (int)a[0], d_in = (int)a[1], d_out = (int)b[0];
-  const paro_status st =
-      GATED ? api.swiglu((int8_t*)q, (float*)sx, (int8_t*)w, (float*)sw, (int8_t*)w2, (float*)s2, (uint16_t*)y, M, d_in, d_out, ty, s)
-            : api.linear((int8_t*)q, (float*)sx, (int8_t*)w, (float*)sw, (uint16_t*)bias, (uint16_t*)y, M, d_in, d_out, ty, s);
-  if (!done(st, GATED ? "paro_w8a8_swiglu" : "paro_w8a8_linear")) return nullptr;
+  if (!(GATED ? run("paro_w8a8_swiglu", api.swiglu, (int8_t*)q, (float*)sx, (int8_t*)w, (float*)sw, (int8_t*)w2, (float*)s2,
+                    (uint16_t*)y, M, d_in, d_out, ty, s)
+              : run("paro_w8a8_linear", api.linear, (int8_t*)q, (float*)sx, (int8_t*)w, (float*)sw, (uint16_t*)bias,
+                    (uint16_t*)y, M, d_in, d_out, ty, s)))
+    return nullptr;
   return Py_NewRef(oy.p);
 }
 
@@ -347,9 +352,9 @@ PyObject* rotate_linear(PyObject*, PyObject* const* v, Py_ssize_t n) {
   }
   Ref ow(output(v[9], t_uint8, 1, &bytes, dev, v[0], "workspace", &ws));
   if (!ow.p || !stream_of(dev, &s)) return nullptr;
-  if (!done(api.rotate((uint16_t*)x, (int)t.K, (uint16_t*)t.pairs, (float*)t.cos, (float*)t.sin, (float*)t.scale, (int8_t*)w,
-                       (float*)sw, (uint16_t*)bias, (uint16_t*)y, (int)a[0], (int)a[1], (int)b[0], ws, (size_t)bytes, s),
-            "paro_rotate_w8a8_linear"))
+  if (!run("paro_rotate_w8a8_linear", api.rotate, (uint16_t*)x, (int)t.K, (uint16_t*)t.pairs, (float*)t.cos, (float*)t.sin,
+           (float*)t.scale, (int8_t*)w, (float*)sw, (uint16_t*)bias, (uint16_t*)y, (int)a[0], (int)a[1], (int)b[0], ws,
+           (size_t)bytes, s))
     return nullptr;
   return Py_NewRef(oy.p);
 }

@@ -1,0 +1,62 @@
+"""The 8-bit calls' native module on the CPU: how it is found and built, and how it
+calls the library.  Every test runs a child process, with stand-ins for torch's
+tensors and the library where it calls."""
+import os
+import subprocess
+import sys
+import textwrap
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def _child(code, **env):
+    p = subprocess.run([sys.executable, "-c", textwrap.dedent(code)], cwd=ROOT, capture_output=True, text=True,
+                       timeout=300, env={**os.environ, **env})
+    assert p.returncode == 0, p.stdout + p.stderr
+    return p.stdout
+
+
+# stand-ins: a tensor whose address is a number of microseconds, and usleep as the
+# library's paro_quantize_activations_int8 (its first argument is x's address)
+FAKES = """
+    import ctypes, threading, time
+    from types import SimpleNamespace
+    import torch
+    import rotation_int4_weight_b200 as paro
+
+    class Tensor:
+        def __init__(self, shape, dtype, at):
+            self.shape, self.dtype, self.device, self.at = torch.Size(shape), dtype, "cuda:0", at
+        def get_device(self): return 0
+        def is_contiguous(self): return True
+        def data_ptr(self): return self.at
+
+    fake = SimpleNamespace(**{n: getattr(torch, n) for n in ("int8", "float32", "bfloat16", "float16", "int16",
+                                                            "uint16", "uint8")},
+                           empty=None, empty_like=None,
+                           _C=SimpleNamespace(_cuda_getCurrentRawStream=lambda d: 0, _cuda_getDevice=lambda: 0))
+    usleep = ctypes.cast(ctypes.CDLL(None).usleep, ctypes.c_void_p).value
+    paro._binding.setup(fake, paro._check, (usleep,) * 7)
+"""
+
+
+def test_other_threads_run_while_the_library_is_called():
+    # a launch that waits for room in the queue must not stop the process's other threads
+    out = _child(FAKES + """
+    ticks, stop = [], False
+    def tick():
+        while not stop:
+            ticks.append(time.perf_counter())
+            time.sleep(0.005)
+    t = threading.Thread(target=tick); t.start()
+    time.sleep(0.05)
+    a = time.perf_counter()
+    paro._binding.quantize(Tensor((2, 16), torch.bfloat16, 400000), Tensor((2, 16), torch.int8, 64),
+                           Tensor((2,), torch.float32, 64))
+    b = time.perf_counter()
+    stop = True; t.join()
+    print(b - a, sum(a < x < b - 0.01 for x in ticks))
+    """)
+    took, ticks = out.split()
+    assert float(took) >= 0.4
+    assert int(ticks) >= 5, "the call kept the interpreter's lock"
