@@ -1,5 +1,5 @@
-"""Builds libparo.so (the C-ABI library) in-tree with nvcc for sm_100a, and _binding.so,
-the 8-bit calls' Python module, with the host compiler.
+"""Builds libparo.so (the C-ABI library) in-tree with nvcc for sm_100a, and _binding, the
+8-bit calls' Python module, with the host compiler.
 
 Usage: python rotation_int4_weight_b200/_build.py [--force] [-v] [--timeline]
 (run it as a file: importing the package would first load the library it builds)
@@ -23,7 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libparo.so")
-BINDING = os.path.join(PKG, "_binding.so")
+# named for the interpreter that it is built for: another one neither loads it nor takes it for built
+BINDING = os.path.join(PKG, "_binding" + sysconfig.get_config_var("EXT_SUFFIX"))
 BUILD_TIMELINE = os.path.join(PKG, "_build_timeline")
 LIB_TIMELINE = os.path.join(PKG, "libparo_timeline.so")
 

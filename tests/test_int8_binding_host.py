@@ -60,3 +60,18 @@ def test_other_threads_run_while_the_library_is_called():
     took, ticks = out.split()
     assert float(took) >= 0.4
     assert int(ticks) >= 5, "the call kept the interpreter's lock"
+
+
+def test_the_module_is_named_for_the_interpreter_it_is_built_for():
+    # a name without a tag would be loaded by any CPython, and count as built for it
+    out = _child("""
+    import importlib.machinery, importlib.util, os, sysconfig
+    import rotation_int4_weight_b200 as paro
+    spec = importlib.util.spec_from_file_location("b", os.path.join(os.path.dirname(paro.__file__), "_build.py"))
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    print(sysconfig.get_config_var("EXT_SUFFIX"), b.BINDING, paro._binding.__file__)
+    """)
+    tag, built, loaded = out.split()
+    assert tag not in (".so", ".abi3.so")
+    assert built == loaded and built.endswith("_binding" + tag)
