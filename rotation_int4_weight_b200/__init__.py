@@ -93,11 +93,22 @@ def _load() -> ctypes.CDLL:
 
 lib = _load()
 
+
+class _NoBinding:
+    """In place of the 8-bit calls' module where it cannot be loaded: they raise, all others work."""
+
+    def __init__(self, cause: ImportError):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("the 8-bit calls need the _binding module, which is missing or not built for this "
+                          "Python: build it with `python rotation_int4_weight_b200/_build.py`") from self._cause
+
+
 try:
     from . import _binding
 except ImportError as e:
-    raise ImportError("the _binding module is missing or not built for this Python: build it with "
-                      "`python rotation_int4_weight_b200/_build.py`") from e
+    _binding = _NoBinding(e)
 
 
 def _check(status: int, what: str) -> None:
@@ -107,9 +118,10 @@ def _check(status: int, what: str) -> None:
         raise ParoError(status, f"{what}: {name}: {msg}")
 
 
-_binding.setup(torch, _check, tuple(ctypes.cast(getattr(lib, n), _P).value for n in (
-    "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
-    "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear")))
+if not isinstance(_binding, _NoBinding):
+    _binding.setup(torch, _check, tuple(ctypes.cast(getattr(lib, n), _P).value for n in (
+        "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
+        "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear")))
 
 
 def _ptr(t: torch.Tensor | None):

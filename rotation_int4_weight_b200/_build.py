@@ -51,12 +51,17 @@ def _newer(target: str, deps: list[str]) -> bool:
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
-def build_binding(force: bool = False, verbose: bool = False) -> str:
-    """The 8-bit calls' Python module: host code only, against Python's headers."""
+def build_binding(force: bool = False, verbose: bool = False) -> str | None:
+    """The 8-bit calls' Python module: host code only, against Python's headers (None without
+    them: the package then has everything but those calls)."""
     src = os.path.join(CSRC, "binding.cpp")
+    include = sysconfig.get_paths()["include"]
     if force or not _newer(BINDING, [src, os.path.join(ROOT, "include", "paro.h")]):
+        if not os.path.exists(os.path.join(include, "Python.h")):
+            print(f"no Python.h in {include}: the 8-bit calls' module is not built", file=sys.stderr, flush=True)
+            return None
         cmd = [os.environ.get("CXX") or shutil.which("g++") or "c++", "-O2", "-std=c++17", "-shared", "-fPIC",
-               "-fvisibility=hidden", "-Wall", "-I", sysconfig.get_paths()["include"], src, "-o", BINDING]
+               "-fvisibility=hidden", "-Wall", "-I", include, src, "-o", BINDING]
         if verbose:
             print(" ".join(cmd), flush=True)
         subprocess.run(cmd, check=True)

@@ -75,3 +75,51 @@ def test_the_module_is_named_for_the_interpreter_it_is_built_for():
     tag, built, loaded = out.split()
     assert tag not in (".so", ".abi3.so")
     assert built == loaded and built.endswith("_binding" + tag)
+
+
+# the package as it is, and a Python that has no _binding for it
+WITHOUT = """
+    import sys
+    class Finder:
+        def find_spec(self, name, path=None, target=None):
+            if name.endswith("._binding"):
+                raise ModuleNotFoundError(f"No module named {name!r}", name=name)
+    sys.meta_path.insert(0, Finder())
+"""
+
+
+def test_the_package_without_the_module_has_everything_but_the_8_bit_calls():
+    _child(WITHOUT + """
+    import torch
+    import rotation_int4_weight_b200 as paro
+    assert paro.paro_weight_layout_version() == 1
+    assert paro.paro_workspace_bytes(1, 512) > 0
+    assert paro.lib.paro_w8a8_linear is not None         # the C ABI has them
+    x = torch.zeros(2, 16, dtype=torch.bfloat16)
+    q, s = torch.zeros(2, 16, dtype=torch.int8), torch.ones(2)
+    for call in (lambda: paro.paro_quantize_activations_int8(x), lambda: paro.paro_rms_norm_int8(x),
+                 lambda: paro.paro_pack_weights_int8(x.float()), lambda: paro.paro_w8a8_linear(q, s, q, s),
+                 lambda: paro.paro_w8a8_swiglu(q, s, q, s, q, s),
+                 lambda: paro.paro_rotate_w8a8_linear(x, None, None, None, None, q, s)):
+        try:
+            call()
+        except ImportError as e:
+            assert "_build.py" in str(e) and isinstance(e.__cause__, ImportError)
+        else:
+            raise AssertionError("the call went on without its module")
+    """)
+
+
+def test_the_build_without_python_headers_leaves_the_module_out():
+    out = _child("""
+    import importlib.util, sys, sysconfig
+    real = sysconfig.get_paths
+    sysconfig.get_paths = lambda *a, **k: dict(real(*a, **k), include="/nonexistent")
+    spec = importlib.util.spec_from_file_location("b", "rotation_int4_weight_b200/_build.py")
+    b = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(b)
+    b._newer = lambda target, deps: False
+    sys.stderr = sys.stdout
+    assert b.build_binding() is None
+    """)
+    assert "Python.h" in out
