@@ -107,9 +107,12 @@ constexpr int kTensorCoreMinM = 128;
 
 // The INT4 linear on x (bf16, or fp16 when x_f16).  With pdl_wait the kernel is
 // launched as a programmatic dependent of the previous kernel in the stream and
-// waits for it before reading x or writing y (the weights may be read earlier,
-// so only a previous kernel that does not write them may trigger early: in this
-// library the INT4 and transform kernels trigger, the weight packing does not).
+// waits for it before reading x or writing y.  The weights may be read earlier,
+// so no kernel that triggers early may write INT4 weights, scales, zeros or a
+// transform's tables.  In this library the INT4 linears, the transforms, the row
+// codes (of weights too: they write int8 codes and their scales) and the int8
+// linears trigger; paro_pack_weights' kernels do not, and a kernel that triggers
+// first of all (the row codes) starts only once such a one is done.
 cudaError_t launch_linear(const uint16_t* x, bool x_f16, const uint32_t* qweight, const uint16_t* scales,
                           const uint16_t* zeros, uint16_t* y, int M, int d_in, int d_out, cudaStream_t s,
                           bool pdl_wait, int* status) {
