@@ -279,10 +279,11 @@ PARO_API paro_status paro_pack_weights_int8(const float* d_W, int d_out, int d_i
 
 /*
  * int8 linear: y[m][n] = sx[m] wscales[n] sum_k q[m][k] qweight[n][k] + bias[n],
- * the sums exact integers, the rest fp32 with one rounding to `dtype`.  d_q: int8
- * [M][d_in], d_in % 16 == 0, d_in <= 49152; d_qweight: int8 [d_out][d_in], any
- * d_out >= 1 (M and d_out at most 2^30); codes may be any int8, -128 among them; d_bias: [d_out] or NULL;
- * d_y: [M][d_out], overlapping no input.  No workspace.
+ * the sums exact integers, the rest fp32 (no product on the way is infinite where
+ * the whole is not) with one rounding to `dtype`.  d_q: int8 [M][d_in], d_in % 16
+ * == 0, d_in <= 49152; d_qweight: int8 [d_out][d_in], any d_out >= 1 (M and d_out at
+ * most 2^30); codes may be any int8, -128 among them; d_bias: [d_out] or NULL; d_y:
+ * [M][d_out], overlapping no input.  No workspace.
  */
 PARO_API paro_status paro_w8a8_linear(const int8_t* d_q, const float* d_sx, const int8_t* d_qweight,
                                       const float* d_wscales, const uint16_t* d_bias, uint16_t* d_y, int M, int d_in,

@@ -195,7 +195,10 @@ __device__ __forceinline__ void commit_pair(uint32_t bar) {
       : "memory");
 }
 
-// 16 or 32 columns of this warp's 32 lanes.
+// 1, 16 or 32 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_ld(uint32_t addr, int& v) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\n" : "=r"(v) : "r"(addr));
+}
 __device__ __forceinline__ void tmem_ld(uint32_t addr, int (&v)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"

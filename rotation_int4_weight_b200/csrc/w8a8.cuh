@@ -35,8 +35,21 @@ bool w8_map(CUtensorMap* map, const int8_t* p, int rows, int d_in, int box_rows)
 // Tensor map of 16-bit y [rows][d_out], d_out a multiple of 8: boxes of 32 x 32, 64-byte swizzle.
 bool w8_out_map(CUtensorMap* map, const uint16_t* y, int rows, int d_out);
 
-__device__ __forceinline__ float w8a8_scaled(int acc, float sx, float sw) {
-  return __fmul_rn(__fmul_rn(__int2float_rn(acc), sx), sw);
+// A token's scale.  A sum (below 2^31) times a scale above 2^97 may pass fp32's
+// range although the channel's scale brings the product back; such a scale is
+// taken 2^-40 of its size and the product 2^40.  Powers of two, so no digit
+// changes; what is smaller by 2^40 on the way is still above 2^50 times the
+// channel's scale.
+struct __align__(8) TokenScale {
+  float s, back;
+};
+__device__ __forceinline__ TokenScale token_scale(float sx) {
+  const bool large = fabsf(sx) > 0x1p+90f;
+  return {large ? sx * 0x1p-40f : sx, large ? 0x1p+40f : 1.0f};
+}
+
+__device__ __forceinline__ float w8a8_scaled(int acc, float s, float sw) {
+  return __fmul_rn(__fmul_rn(__int2float_rn(acc), s), sw);
 }
 
 // silu(g) * u.  exp(-g) overflows to infinity for g < -88, where the quotient

@@ -84,7 +84,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   __shared__ __align__(8) uint64_t bars[2 * kMaxStages + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag, s_issued, s_committed;
-  __shared__ float s_sx[TN];
+  __shared__ TokenScale s_sx[TN];
 
   unsigned char* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const uint32_t ring = smem_u32(smem);
@@ -194,7 +194,7 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   const int n = n0 + 4 * lane;  // this lane's channels n .. n + 3, of warp - 2, warp + 2, ...'s tokens
   float sw[NW][4], bias[4];
   if (warp >= 2) {
-    for (int t = threadIdx.x - 64; t < tokens; t += kRows) s_sx[t] = A.sx[m0 + t];
+    for (int t = threadIdx.x - 64; t < tokens; t += kRows) s_sx[t] = token_scale(A.sx[m0 + t]);
     asm volatile("bar.sync 1, 128;\n" ::: "memory");
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -241,13 +241,13 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
           sum[g][2] += part[g][r].z;
           sum[g][3] += part[g][r].w;
         }
-    const float sx = s_sx[t];
+    const TokenScale sx = s_sx[t];
     uint32_t o[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float v = w8a8_scaled(sum[0][e], sx, sw[0][e]);
-      if constexpr (GATED) v = w8a8_gate(v, w8a8_scaled(sum[NW - 1][e], sx, sw[NW - 1][e]));
-      else v += bias[e];
+      float v = w8a8_scaled(sum[0][e], sx.s, sw[0][e]);
+      if constexpr (GATED) v = w8a8_gate(v * sx.back, w8a8_scaled(sum[NW - 1][e], sx.s, sw[NW - 1][e]) * sx.back);
+      else v = __fmaf_rn(v, sx.back, bias[e]);
       o[e] = to_16<F16>(v);
     }
     uint16_t* dst = A.y + (size_t)(m0 + t) * A.d_out + n;

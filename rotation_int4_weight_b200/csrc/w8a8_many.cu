@@ -177,7 +177,8 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
     for (int t = pair; t < A.tiles; t += pairs, ++j) {
       const int acc = j & 1;
       const int m_warp = (t % A.mtiles) * kTile + rank * kHalf + quarter * 32, m = m_warp + lane, n0 = (t / A.mtiles) * NC;
-      const float sx = m < A.M ? A.sx[m] : 0.0f;
+      const TokenScale sx = token_scale(m < A.M ? A.sx[m] : 0.0f);
+      const bool any_large = __any_sync(0xffffffffu, sx.back != 1.0f);
       // the tile's channel values, while its MMAs run; two sets, so that a warp
       // may be one tile ahead of another
       for (int c = threadIdx.x - 64; c < kTile; c += 32 * kEpiWarps) {
@@ -205,17 +206,18 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
 #pragma unroll
         for (int c = 0; c < 32; c += 4) {
           const float4 w = *reinterpret_cast<const float4*>(&s_sw[acc][c0 + c]);
-          float f[4] = {w8a8_scaled(v[c], sx, w.x), w8a8_scaled(v[c + 1], sx, w.y), w8a8_scaled(v[c + 2], sx, w.z),
-                        w8a8_scaled(v[c + 3], sx, w.w)};
+          float f[4] = {w8a8_scaled(v[c], sx.s, w.x), w8a8_scaled(v[c + 1], sx.s, w.y), w8a8_scaled(v[c + 2], sx.s, w.z),
+                        w8a8_scaled(v[c + 3], sx.s, w.w)};
           if constexpr (GATED) {
             const float4 w2 = *reinterpret_cast<const float4*>(&s_sw[acc][kHalf + c0 + c]);
-            f[0] = w8a8_gate(f[0], w8a8_scaled(u[c], sx, w2.x));
-            f[1] = w8a8_gate(f[1], w8a8_scaled(u[c + 1], sx, w2.y));
-            f[2] = w8a8_gate(f[2], w8a8_scaled(u[c + 2], sx, w2.z));
-            f[3] = w8a8_gate(f[3], w8a8_scaled(u[c + 3], sx, w2.w));
+            f[0] = w8a8_gate(f[0], w8a8_scaled(u[c], sx.s, w2.x));
+            f[1] = w8a8_gate(f[1], w8a8_scaled(u[c + 1], sx.s, w2.y));
+            f[2] = w8a8_gate(f[2], w8a8_scaled(u[c + 2], sx.s, w2.z));
+            f[3] = w8a8_gate(f[3], w8a8_scaled(u[c + 3], sx.s, w2.w));
           } else {
             const float4 b = *reinterpret_cast<const float4*>(&s_bias[acc][c0 + c]);
-            f[0] += b.x, f[1] += b.y, f[2] += b.z, f[3] += b.w;
+            f[0] = __fmaf_rn(f[0], sx.back, b.x), f[1] = __fmaf_rn(f[1], sx.back, b.y);
+            f[2] = __fmaf_rn(f[2], sx.back, b.z), f[3] = __fmaf_rn(f[3], sx.back, b.w);
           }
           o[c / 2] = to_16<F16>(f[0]) | ((uint32_t)to_16<F16>(f[1]) << 16);
           o[c / 2 + 1] = to_16<F16>(f[2]) | ((uint32_t)to_16<F16>(f[3]) << 16);
@@ -229,6 +231,20 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
         for (int i = 0; i < 4; ++i)
           *reinterpret_cast<uint4*>(box + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
               make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        if (GATED && any_large) {
+          // tokens of large scales once more, with the factor that a gate cannot take
+          // later (two multiplications for every output would cost 3% of a short call)
+#pragma unroll 1
+          for (int c = 0; c < 32; ++c) {
+            int g1, u1;
+            tmem_ld(lanes + acc * kTile + c0 + c, g1);
+            tmem_ld(lanes + acc * kTile + kHalf + c0 + c, u1);
+            tmem_ld_wait();
+            const float f = w8a8_gate(w8a8_scaled(g1, sx.s, s_sw[acc][c0 + c]) * sx.back,
+                                      w8a8_scaled(u1, sx.s, s_sw[acc][kHalf + c0 + c]) * sx.back);
+            *reinterpret_cast<uint16_t*>(box + lane * 64 + (((c >> 3) ^ ((lane >> 1) & 3)) << 4) + (c & 7) * 2) = to_16<F16>(f);
+          }
+        }
         if (by_tma) {
           async_fence();
           __syncwarp();
