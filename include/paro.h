@@ -291,7 +291,8 @@ PARO_API paro_status paro_w8a8_linear(const int8_t* d_q, const float* d_sx, cons
 
 /*
  * Gated pair of int8 linears in one kernel: y = silu(g) * u with g and u the two
- * products of paro_w8a8_linear (no bias), silu(g) = g / (1 + exp(-g)) in fp32;
+ * products of paro_w8a8_linear (no bias), silu(g) = g / (1 + exp(-g)) in fp32, 0
+ * for g below -87.3 (where |silu(g)| < 1.2e-36);
  * neither g nor u is rounded or written.  Arguments as paro_w8a8_linear.
  */
 PARO_API paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t* d_gate_qweight,

@@ -52,10 +52,12 @@ __device__ __forceinline__ float w8a8_scaled(int acc, float s, float sw) {
   return __fmul_rn(__fmul_rn(__int2float_rn(acc), s), sw);
 }
 
-// silu(g) * u.  exp(-g) overflows to infinity for g < -88, where the quotient
-// is the right -0; fast exp and divide are within 1e-5 of g / (1 + exp(-g))
-// wherever that is not below fp32's smallest values, far inside half a step of
-// the 16-bit result (bf16 2^-9, fp16 2^-12).
+// silu(g) * u.  Fast exp and divide are within 2e-5 of g / (1 + exp(-g)), far inside
+// half a step of the 16-bit result (bf16 2^-9, fp16 2^-12), for g above -87.3.  Below,
+// the divisor passes 2^126, for which the fast quotient is -0: silu(g) is then taken
+// as 0, at most 1.1e-36 off.  (Both sides a quarter of their size keep the divisor
+// below 2^126, which brings values down to 2.7e-37 back, and cost 3% of a gated call of
+// 128-1024 tokens 1536 -> 8960: 12.06 us for 11.73.)
 __device__ __forceinline__ float w8a8_gate(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
