@@ -342,10 +342,15 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
 // two launches at once must never wait for each other.  They cannot, because the
 // CTAs that an SM's shared memory lets in never want more than its 512 columns,
 // and one that takes all 512 (w8a8_many, w4_tc) leaves no shared memory for another.
+// Other libraries' kernels on pairs of SMs wait for columns too.  They fill shared
+// memory; a CTA here asks for 72 KB at least, so that none with more than 155 KB fits
+// beside it (28 KB, where a share is one step, left room for one of 199).
+constexpr int kLeastSmem = 72 * 1024;
 template <int TN, bool GATED>
 constexpr int least_smem() {
   using Geo = FewGeo<TN, GATED>;
-  return 1024 + (Geo::STORED ? Geo::STAGE + Geo::SUMS : Geo::STAGE > Geo::SUMS ? Geo::STAGE : Geo::SUMS);
+  const int used = 1024 + (Geo::STORED ? Geo::STAGE + Geo::SUMS : Geo::STAGE > Geo::SUMS ? Geo::STAGE : Geo::SUMS);
+  return used > kLeastSmem ? used : kLeastSmem;
 }
 
 template <int TN, bool GATED, bool F16>
@@ -353,7 +358,6 @@ cudaError_t launch_few(FewArgs& A, const W8a8Few& f, int* status, cudaStream_t s
   using Geo = FewGeo<TN, GATED>;
   constexpr int kSmSmem = 228 * 1024;
   static_assert(kSmSmem / least_smem<TN, GATED>() * Geo::COLS <= 512, "tensor memory of the CTAs that fit an SM");
-  static_assert(least_smem<TN, GATED>() > 16 * 1024, "no room beside a CTA with all of tensor memory");
   const int per = (A.blocks + f.split - 1) / f.split;
   A.split = f.split;
   constexpr int kBudget = 104 * 1024;  // of 228 KB, for two CTAs
@@ -367,6 +371,7 @@ cudaError_t launch_few(FewArgs& A, const W8a8Few& f, int* status, cudaStream_t s
   A.stages = stages;
   A.hooks = w8a8_hooks(f.split);
   bytes += 1024;
+  if (bytes < kLeastSmem) bytes = kLeastSmem;
   auto kernel = w8a8_few_kernel<TN, GATED, F16>;
   static std::atomic<uint64_t> limit{0};
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kernel), kMaxSmem, limit);

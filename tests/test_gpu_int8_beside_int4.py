@@ -123,3 +123,46 @@ def test_int4_calls_between_8_bit_calls_in_a_graph(M):
             assert all(torch.equal(a, b) for a, b in zip(c.results(), alone))
         c.check_first_layer()
     _status_ok()
+
+
+def _fork_and_join(side, x, Wm):
+    """Codes of Wm on a side stream, codes of x on the current one, then the linear of both
+    and the codes of its output on the side stream: the join gives the linear two kernels to wait for."""
+    main = torch.cuda.current_stream()
+    side.wait_stream(main)
+    w, sw = paro.paro_quantize_activations_int8(Wm, stream=side)
+    q, sx = paro.paro_quantize_activations_int8(x)
+    main.wait_stream(side)
+    y = paro.paro_w8a8_linear(q, sx, w, sw)
+    side.wait_stream(main)
+    z, sz = paro.paro_quantize_activations_int8(y, stream=side)
+    main.wait_stream(side)
+    return q, sx, w, sw, y, z, sz
+
+
+@pytest.mark.parametrize("M", [2, 64, 700])
+def test_a_linear_that_joins_two_streams(M):
+    # the codes of a large matrix take 10 times those of x, so the linear may not go by the kernel
+    # before it on its own stream alone; eagerly and in a graph
+    x = _acts(M, 4096, BF16, 1, spread=False)
+    Wm = _acts(8960, 4096, BF16, 2, spread=False)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = _fork_and_join(side, x, Wm)
+    for seed in range(4):
+        x.copy_(_acts(M, 4096, BF16, 10 + seed, spread=False))
+        Wm.copy_(_acts(8960, 4096, BF16, 20 + seed, spread=False))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        eager = _fork_and_join(side, x, Wm)
+        _status_ok()
+        for got in (held, eager):
+            q, sx, w, sw, y, z, sz = got
+            assert_linear(y, q, sx, w, sw)
+            assert torch.equal(z, paro.paro_quantize_activations_int8(y)[0])
+            assert torch.equal(q, paro.paro_quantize_activations_int8(x)[0])
+            assert torch.equal(w, paro.paro_quantize_activations_int8(Wm)[0])
+        assert all(torch.equal(a, b) for a, b in zip(held, eager))
