@@ -508,12 +508,12 @@ PARO_API paro_status paro_get_device_status(paro_stream_t stream);
  * waits run out: the call then reports PARO_ERR_TIMEOUT through
  * paro_get_device_status() and writes none of the output tiles of the linears
  * it waited for.  In the int8 linears it makes the last CTA of every cluster
- * (the first, where skip_ready_flags is 2) stop its copies after the first 128
- * columns of its share of d_in, so that the waits for the others run out: the
- * call reports PARO_ERR_TIMEOUT and writes no tile that such a CTA has a share
- * in, if that share is longer.  Nothing hangs: these waits are bounded.  Not thread-safe with
- * respect to calls being configured at the same time; PARO_ERR_INVALID_ARG
- * for a negative cycle count.
+ * (the first, where skip_ready_flags is 2) stop its copies when its ring of at
+ * most 8 stages of 128 columns of d_in is full, so that the waits for the others
+ * run out: the call reports PARO_ERR_TIMEOUT and writes no tile that such a CTA
+ * has a share in, if that share is longer.  Nothing hangs: these waits are
+ * bounded.  Not thread-safe with respect to calls being configured at the same
+ * time; PARO_ERR_INVALID_ARG for a negative cycle count.
  */
 PARO_API paro_status paro_set_test_hooks(long long flag_wait_cycles, int skip_ready_flags);
 

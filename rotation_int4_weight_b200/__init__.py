@@ -460,7 +460,7 @@ def paro_set_test_hooks(flag_wait_cycles: int = 0, skip_ready_flags: bool | int 
     flag waits and the int8 linears' waits to `flag_wait_cycles` SM cycles (0: the
     default, about a second), make the decode transforms skip publishing their
     flags, and make the last CTA of every cluster of the int8 linears (2: the
-    first) stop copying after one step.  Affects the calls configured afterwards;
+    first) stop copying when its ring is full.  Affects the calls configured afterwards;
     (0, False) restores the defaults."""
     _check(lib.paro_set_test_hooks(int(flag_wait_cycles), int(skip_ready_flags or 0)), "paro_set_test_hooks")
 

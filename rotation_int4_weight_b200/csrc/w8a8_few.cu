@@ -140,14 +140,16 @@ w8a8_few_kernel(const __grid_constant__ FewArgs A, int* status) {
   // 800 clocks, which held every SM to 40 GB/s.
   if (warp == 0) {
     if (lane == 0) {
-      const int copied = rank == A.hooks.rank && nk > 1 ? 1 : nk;
       int i = 0, s = 0, x = k0 * kK;
       uint32_t phase = 1, dst = ring, bar = b_full;
       bool ok = true;
 #pragma unroll 1
-      for (; i < copied; ++i, x += kK) {
+      for (; i < nk; ++i, x += kK) {
         // (phase starts at 1: the first wait, a round later, is for parity 0)
-        if (i >= stages && !wait(bar + (b_empty - b_full), phase)) { fail(); ok = false; break; }
+        if (i >= stages) {
+          if (rank == A.hooks.rank) { ok = false; break; }
+          if (!wait(bar + (b_empty - b_full), phase)) { fail(); ok = false; break; }
+        }
         mbar_expect_tx(bar, (NW * kRows + A.xrows) * kK);
         tma_load(dst, &A.w, x, n0, bar);
         if constexpr (GATED) tma_load(dst + kRows * kK, &A.w2, x, n0, bar);

@@ -22,8 +22,6 @@
 // run under a tile's epilogue.  Every wait on an mbarrier is bounded; when one runs
 // out, the roles of both CTAs end, their copies and MMAs in flight are waited for,
 // and the call reports PARO_ERR_TIMEOUT.
-#include <climits>
-
 #include "int8.cuh"
 #include "tc_ptx.cuh"
 #include "w4_stream.cuh"  // device_sm_count
@@ -118,14 +116,16 @@ w8a8_many_kernel(const __grid_constant__ ManyArgs A, int* status) {
       int it = 0, s = 0;
       uint32_t phase = 1;
       bool ok = true;
-      const int copied = rank == A.hooks.rank ? 1 : INT_MAX;
 #pragma unroll 1
-      for (int t = pair; ok && it < copied && t < A.tiles; t += pairs) {
+      for (int t = pair; ok && t < A.tiles; t += pairs) {
         const int m0 = (t % A.mtiles) * kTile + rank * kHalf;
         const int n0 = (t / A.mtiles) * NC + (GATED ? 0 : rank * kHalf);
 #pragma unroll 1
-        for (int x = 0; x < A.blocks * kK && it < copied; x += kK, ++it) {
-          if (it >= kStages && !wait(b_empty + 8 * s, phase)) { fail(); ok = false; break; }
+        for (int x = 0; x < A.blocks * kK; x += kK, ++it) {
+          if (it >= kStages) {
+            if (rank == A.hooks.rank) { ok = false; break; }
+            if (!wait(b_empty + 8 * s, phase)) { fail(); ok = false; break; }
+          }
           const uint32_t bar = first + 8 * s, dst = ring + s * kStageBytes;
           if (rank == 0) mbar_expect_tx(b_full + 8 * s, 2 * kStageBytes);
           tma_load_pair(dst, &A.q, x, m0, bar);

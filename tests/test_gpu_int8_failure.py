@@ -1,7 +1,7 @@
 """Waits of the int8 linears that run out, on the GPU without a fault (needs a B200).
 
 The test hook paro_set_test_hooks makes one CTA of every cluster stop its copies
-after the first stage and bounds the waits to a fraction of a millisecond.  The
+when its ring is full and bounds the waits to a fraction of a millisecond.  The
 call then has to end with PARO_ERR_TIMEOUT, write nothing, and leave the context
 usable: its copies and MMAs in flight are waited for, also where the two CTAs of
 a pair have sent different numbers of stages.
@@ -17,8 +17,9 @@ paro = pytest.importorskip("rotation_int4_weight_b200")
 TIMEOUT = 4
 
 # sums stored into their owners, sums read between cluster barriers, pairs of CTAs
-# (one tile a pair, several)
-SHAPES = [(1, 4096, 1024), (20, 14336, 1000), (100, 4096, 1024), (200, 4096, 1536), (1500, 2064, 2048), (2081, 1040, 8960)]
+# (one tile a pair, several); shares of d_in longer than a ring, so that copies stop
+SHAPES = [(1, 14336, 1024), (20, 14336, 1000), (64, 14336, 2000), (100, 14336, 1024), (200, 14336, 1536), (1500, 2064, 2048),
+          (2081, 1040, 8960)]
 
 
 @pytest.mark.parametrize("gated", [False, True])
