@@ -259,7 +259,9 @@ PARO_API paro_status paro_quantize_activations_int8(const uint16_t* d_x, int8_t*
  * of v_c = h_c gain_c / sqrt(mean_c h_c^2 + eps), v not rounded before its codes
  * (products h_c gain_c in fp32: exact, unless they leave fp32's range).
  * d_gain: [d], NULL meaning ones; eps >= 0.  d_hidden may be d_x or d_residual
- * (in place); other overlaps with outputs are refused.
+ * (in place); other overlaps with outputs are refused.  The codes are for linears
+ * without a transform: the normalised row itself, which a transform takes, is not
+ * given.
  */
 PARO_API paro_status paro_rms_norm_int8(const uint16_t* d_x, const uint16_t* d_residual, const uint16_t* d_gain,
                                         float eps, uint16_t* d_hidden, int8_t* d_q, float* d_sx, int M, int d,
@@ -293,7 +295,9 @@ PARO_API paro_status paro_w8a8_linear(const int8_t* d_q, const float* d_sx, cons
  * Gated pair of int8 linears in one kernel: y = silu(g) * u with g and u the two
  * products of paro_w8a8_linear (no bias), silu(g) = g / (1 + exp(-g)) in fp32, 0
  * for g below -87.3 (where |silu(g)| < 1.2e-36);
- * neither g nor u is rounded or written.  Arguments as paro_w8a8_linear.
+ * neither g nor u is rounded or written.  Arguments as paro_w8a8_linear.  Both
+ * products take the same codes: weights with a transform folded in need one that
+ * gate and up share.
  */
 PARO_API paro_status paro_w8a8_swiglu(const int8_t* d_q, const float* d_sx, const int8_t* d_gate_qweight,
                                       const float* d_gate_wscales, const int8_t* d_up_qweight,

@@ -22,10 +22,13 @@
 // multiples of 16 of the flat index, not of the column, so that rows of an odd
 // width still move as 16-byte loads and stores; the first and last chunk of such
 // a row go value by value, and its gain comes from aligned 16-byte loads shifted
-// by the row's phase.  For many rows the instructions, about 14 a value, and HBM
-// bound it alike: 2048 x 4096 bf16 with a residual in 13.7 us (4.3 TB/s), 4096 x
-// 8192 in 43.7 us (5.4 TB/s), packing 14336 x 4096 fp32 in 44.4 us (6.6 TB/s);
-// for one row its latency does (2.5 us).
+// by the row's phase.  For many rows HBM bounds it: added rows come at its rate
+// (norm with a residual, 4096 wide: 4096 more rows in 18.8 us, 6.2 TB/s; codes, 14336
+// wide: 2048 more in 13.5 us, 6.5 TB/s), and the instructions, about 14 a value, fill
+// 37% of the issue slots.  A call has 4 us (norm) to 8 us (codes) around that, for the
+// launch, the first rows' loads with nothing to compute yet, and the last rows: 2048 x
+// 4096 with a residual in 13.7 us (4.3 TB/s), 4096 x 8192 in 43.7 us (5.4 TB/s), packing
+// 14336 x 4096 fp32 in 44-45 us (6.6 TB/s).  One row's latency is 2.5 us.
 #include "int8.cuh"
 #include "tc_ptx.cuh"
 #include "w4_stream.cuh"  // device_sm_count

@@ -21,9 +21,9 @@
 // nothing to reset between calls.
 //
 // Bound by the weights from HBM and about 3 us of set-up, first loads and shares'
-// sums around them: one token 4096 -> 14336 in 13.5 us (58.7 MB, 4.4 TB/s), 14336 ->
-// 4096 in 13.3 us, gated 4096 -> 14336 in 22.7 us (5.2 TB/s), 1536 -> 1536 in 3.5 us;
-// between 4096 -> 4096 and 14336 -> 4096 the added bytes come at 6.0 TB/s.
+// sums around them: one token 4096 -> 14336 in 13.5 us (58.7 MB, 4.3 TB/s), 14336 ->
+// 4096 in 13.2-13.6 us, gated 4096 -> 14336 in 22.6 us (5.2 TB/s), 1536 -> 1536 in 3.4
+// us; between 4096 -> 4096 and 14336 -> 4096 the added bytes come at 5.9 TB/s.
 //
 // The launch overlaps the kernel before it: until that one is done a CTA sets up
 // its barriers and asks for its weights in L2 only, which is right whoever wrote

@@ -16,8 +16,8 @@
 // A 256 x 256 tile on a pair reads each operand once for both SMs' tensor cores, 32
 // KB an SM for 512 clocks of MMAs; a 128 x 256 tile on one SM would read 48.
 // Bound by the tensor cores under the power cap, and by the last round of tiles:
-// 2048 tokens 14336 -> 4096 in 84.5 us (2.85 PFLOP/s; 99 us when it runs for
-// seconds), gated 4096 -> 14336 in 164 us (2.93).
+// 2048 tokens 14336 -> 4096 in 85 us (2.83 PFLOP/s; 98 us when it runs for
+// seconds), gated 4096 -> 14336 in 166 us (2.90).
 // Two sets of sums (2 x 256 columns of tensor memory) let the next tile's MMAs
 // run under a tile's epilogue.  Every wait on an mbarrier is bounded; when one runs
 // out, the roles of both CTAs end, their copies and MMAs in flight are waited for,
