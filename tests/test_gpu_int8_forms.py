@@ -63,3 +63,24 @@ def test_ragged_last_token_tile_among_many_tiles_a_pair(M):
         assert torch.equal(again, y)
         again = paro.paro_w8a8_swiglu(q, sx, w, sw * 20, w2, s2 * 20, out_dtype=FP16)
         assert torch.equal(again, z)
+
+
+@pytest.mark.parametrize("t", [BF16, FP16])
+@pytest.mark.parametrize("d_in,d_out", [(4096, 1536), (528, 4098), (2064, 5001)])
+def test_a_token_does_not_depend_on_the_form_that_takes_it(d_in, d_out, t):
+    # the same rows of q alone, in small calls and in large ones: bit for bit
+    M = 2100
+    q, sx, w, sw, w2, s2, b = _operands(M, d_in, d_out, 11)
+    sx[7] = 2.0 ** 100
+    b, sw, s2 = b.to(t), sw * 20, s2 * 20
+    y = paro.paro_w8a8_linear(q, sx, w, sw, b, out_dtype=t)
+    z = paro.paro_w8a8_swiglu(q, sx, w, sw, w2, s2, out_dtype=t)
+    forms = {paro.paro_w8a8_form(M, d_in, d_out)}
+    for lo, n in ((7, 1), (0, 16), (40, 33), (512, 100), (0, 300), (2099, 1), (1024, 700)):
+        rows = slice(lo, lo + n)
+        qs, ss = q[rows].contiguous(), sx[rows].contiguous()
+        assert torch.equal(paro.paro_w8a8_linear(qs, ss, w, sw, b, out_dtype=t), y[rows])
+        assert torch.equal(paro.paro_w8a8_swiglu(qs, ss, w, sw, w2, s2, out_dtype=t), z[rows])
+        forms.add(paro.paro_w8a8_form(n, d_in, d_out))
+    _status_ok()
+    assert len(forms) >= 4
