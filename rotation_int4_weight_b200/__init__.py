@@ -94,23 +94,6 @@ def _load() -> ctypes.CDLL:
 lib = _load()
 
 
-class _NoBinding:
-    """In place of the 8-bit calls' module where it cannot be loaded: they raise, all others work."""
-
-    def __init__(self, cause: ImportError):
-        self._cause = cause
-
-    def __getattr__(self, name):
-        raise ImportError("the 8-bit calls need the _binding module, which is missing or not built for this "
-                          "Python: build it with `python rotation_int4_weight_b200/_build.py`") from self._cause
-
-
-try:
-    from . import _binding
-except ImportError as e:
-    _binding = _NoBinding(e)
-
-
 def _check(status: int, what: str) -> None:
     if status != 0:
         name = lib.paro_status_string(status).decode()
@@ -118,10 +101,25 @@ def _check(status: int, what: str) -> None:
         raise ParoError(status, f"{what}: {name}: {msg}")
 
 
-if not isinstance(_binding, _NoBinding):
+class _NoBinding:
+    """In place of the 8-bit calls' module where it cannot be used: they raise, all others work."""
+
+    def __init__(self, cause: Exception):
+        self._cause = cause
+
+    def __getattr__(self, name):
+        raise ImportError("the 8-bit calls need the _binding module, which is missing, not built for this Python or "
+                          f"without what it needs of torch ({self._cause}): build it with "
+                          "`python rotation_int4_weight_b200/_build.py`") from self._cause
+
+
+try:
+    from . import _binding
     _binding.setup(torch, _check, tuple(ctypes.cast(getattr(lib, n), _P).value for n in (
         "paro_quantize_activations_int8", "paro_rms_norm_int8", "paro_pack_weights_int8", "paro_w8a8_linear",
         "paro_w8a8_swiglu", "paro_rotate_w8a8_workspace_bytes", "paro_rotate_w8a8_linear")))
+except (ImportError, AttributeError) as e:  # AttributeError: a torch without CUDA
+    _binding = _NoBinding(e)
 
 
 def _ptr(t: torch.Tensor | None):

@@ -110,6 +110,21 @@ def test_the_package_without_the_module_has_everything_but_the_8_bit_calls():
     """)
 
 
+def test_the_package_imports_with_a_torch_that_has_no_cuda():
+    _child("""
+    import torch
+    del torch._C._cuda_getCurrentRawStream
+    import rotation_int4_weight_b200 as paro
+    assert paro.paro_workspace_bytes(1, 512) > 0
+    try:
+        paro.paro_quantize_activations_int8(torch.zeros(2, 16, dtype=torch.bfloat16))
+    except ImportError as e:
+        assert "_cuda_getCurrentRawStream" in str(e)
+    else:
+        raise AssertionError("the call went on")
+    """)
+
+
 def test_the_build_without_python_headers_leaves_the_module_out():
     out = _child("""
     import importlib.util, sys, sysconfig
